@@ -24,6 +24,12 @@ __all__ = [
     "hq_group_contiguous_gemm_dswiglu", "hq_group_contiguous_gemm_dswiglu_quant",
     "hq_prefill_permute_to_masked_gemm", "prefill_permute_to_masked_gemm",
     "HQ_SCALE_BROADCAST", "HQ_SCALE_DIRECT",
+    "HQ_BLOCK_2D", "HQ_TRANSPOSE", "HQ_OUT_FP32", "HQ_ACCUMULATE", "HQ_BLOCK_WORKSPACE_BYTES",
+    "HQ_SORT_WORKSPACE_BYTES", "hq_block_quant", "hq_fused_swiglu_block_quant", "hq_block_gemm",
+    "hq_block_gemm_workspace_size", "hq_block_group_contiguous_gemm", "hq_block_group_masked_gemm",
+    "hq_block_group_k_gemm", "hq_moe_sort", "hq_moe_sort_workspace_size", "hq_moe_permute",
+    "hq_moe_permute_block_quant", "hq_moe_combine", "hq_moe_combine_backward",
+    "block_quantize", "moe_max_rows", "moe_sort",
     "hq_last_error", "library_path", "load", "EXPORTED_SYMBOLS",
     "quantize", "group_size", "code_cols",
 ]
@@ -36,6 +42,12 @@ HQ_IN_FP16 = 2
 HQ_OUT_FP16 = 0x100      # OR'ed into a GEMM's mode: out is float16, not bfloat16
 HQ_SCALE_BROADCAST = 0
 HQ_SCALE_DIRECT = 1
+HQ_BLOCK_2D = 4          # hq_block_quant: 128 x 128 blocks
+HQ_TRANSPOSE = 8         # hq_block_quant: codes and scales of the transpose
+HQ_OUT_FP32 = 0x200      # block products: float32 out
+HQ_ACCUMULATE = 0x400    # block products: added to a float32 out
+HQ_BLOCK_WORKSPACE_BYTES = 64 << 20   # no hq_block_gemm call uses more
+HQ_SORT_WORKSPACE_BYTES = 1 << 20     # no hq_moe_sort call uses more
 
 MODES = {"mxfp8": HQ_MXFP8, "mxfp4": HQ_MXFP4, "nvfp4": HQ_NVFP4,
          "w8a8-mxfp8": HQ_MXFP8, "w4a4-mxfp4": HQ_MXFP4, "w4a4-nvfp4": HQ_NVFP4}
@@ -47,6 +59,10 @@ EXPORTED_SYMBOLS = (
     "hq_group_contiguous_gemm_swiglu_quant", "hq_group_contiguous_gemm_ptr_array",
     "hq_prefill_permute_to_masked_gemm", "hq_group_contiguous_gemm_dswiglu",
     "hq_group_contiguous_gemm_dswiglu_quant",
+    "hq_block_quant", "hq_fused_swiglu_block_quant", "hq_block_gemm", "hq_block_gemm_workspace_size",
+    "hq_block_group_contiguous_gemm", "hq_block_group_masked_gemm", "hq_block_group_k_gemm",
+    "hq_moe_sort", "hq_moe_sort_workspace_size", "hq_moe_permute", "hq_moe_permute_block_quant",
+    "hq_moe_combine", "hq_moe_combine_backward",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -96,6 +112,21 @@ _SIGS = {
                                _VP, _VP], _I32),
     "hq_prefill_permute_to_masked_gemm": ([_VP, _VP, _I64, _I64, _I64, _VP, _I32, _VP, _I32, _I32,
                                            _I64, _VP, _VP, _VP, _VP], _I32),
+    "hq_block_quant": ([_VP, _VP, _I64, _I64, _I64, _VP, _VP, _U32], _I32),
+    "hq_fused_swiglu_block_quant": ([_VP, _VP, _I64, _I64, _VP, _I32, _VP, _VP, _U32], _I32),
+    "hq_block_gemm": ([_VP, _U32, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I64, _VP, _U64], _I32),
+    "hq_block_gemm_workspace_size": ([_U32, _I64, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_uint64)], _I32),
+    "hq_block_group_contiguous_gemm": ([_VP, _U32, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _I64, _I64, _I64], _I32),
+    "hq_block_group_masked_gemm": ([_VP, _U32, _VP, _VP, _VP, _VP, _VP, _I32, _I64, _VP, _I64, _I64], _I32),
+    "hq_block_group_k_gemm": ([_VP, _U32, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _I64, _I64, _I64], _I32),
+    "hq_moe_sort": ([_VP, _VP, _I64, _I32, _I32, _I32, _I64, _VP, _VP, _VP, _VP, _VP, _U64], _I32),
+    "hq_moe_sort_workspace_size": ([_I64, _I32, _I32, ctypes.POINTER(ctypes.c_uint64)], _I32),
+    "hq_moe_permute": ([_VP, _VP, _I64, _I64, _VP, _I32, _VP, _VP, _I32, _I64, _VP], _I32),
+    "hq_moe_permute_block_quant": ([_VP, _VP, _I64, _I64, _VP, _I32, _VP, _VP, _I32, _I64, _VP, _VP, _U32],
+                                   _I32),
+    "hq_moe_combine": ([_VP, _VP, _I64, _I64, _VP, _I32, _VP, _I64, _VP, _U32], _I32),
+    "hq_moe_combine_backward": ([_VP, _VP, _VP, _I64, _I64, _VP, _I32, _VP, _VP, _VP, _I32, _I64, _VP, _VP,
+                                 _U32], _I32),
 }
 
 
@@ -497,6 +528,274 @@ def prefill_permute_to_masked_gemm(x, scale, topk_ids, num_local_experts, max_to
     nums = torch.empty((E, 1), dtype=torch.int32, device=dev)
     hq_prefill_permute_to_masked_gemm(x, scale, topk_ids, E, M, px, osf, imap, nums, hidden)
     return px, osf, imap, nums
+
+
+# ---------------------------------------------------------------- block-128 FP8
+# Small calls are launch-bound, so the calls below check each argument once and
+# pass plain integers.
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _arg(t, name, dtype, numel):
+    """The address of a contiguous device tensor of this dtype and size."""
+    if t.dtype is not dtype or t.numel() != numel or not t.is_cuda or not t.is_contiguous():
+        _need(t, name, dtype, numel)
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, numel):
+    return None if t is None else _arg(t, name, dtype, numel)
+
+
+def _half(t, name, numel, like=None):
+    """The address of a bfloat16 or float16 tensor (of `like`'s dtype)."""
+    if t.dtype not in _HALVES:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return _arg(t, name, t.dtype if like is None else like.dtype, numel)
+
+
+def _raw_stream(t):
+    """The current HIP stream of t's device."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("tensors must be device tensors")
+    return torch._C._cuda_getCurrentRawStream(d)
+
+
+def _in_flag(t):
+    return HQ_IN_FP16 if t.dtype is torch.float16 else 0
+
+
+_OUT_FLAGS = {torch.bfloat16: 0, torch.float16: HQ_OUT_FP16, torch.float32: HQ_OUT_FP32}
+
+
+def _out(out, numel, accumulate):
+    """The address of a product's output and the flags for its dtype."""
+    flags = _OUT_FLAGS.get(out.dtype)
+    if flags is None:
+        raise ValueError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
+    if accumulate:
+        if out.dtype is not torch.float32:
+            raise ValueError("accumulate needs a float32 out")
+        flags |= HQ_ACCUMULATE
+    return _arg(out, "out", out.dtype, numel), flags
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def hq_block_quant(x, q, sf, block_2d=False, transpose=False):
+    """x [.., m, k] (2-D, or 3-D with a batch) bfloat16 or float16 -> E4M3 codes
+    q uint8 [.., m, k] and scales sf float32 [.., m, ceil(k/128)] in place; with
+    block_2d one scale per 128 x 128 block; with transpose q [.., k, m] and sf
+    hold the transpose's codes and blocks."""
+    m, k = x.shape[-2:]
+    batch = x.shape[0] if x.dim() == 3 else 1
+    rows, cols = (k, m) if transpose else (m, k)
+    flags = _in_flag(x) | (HQ_BLOCK_2D if block_2d else 0) | (HQ_TRANSPOSE if transpose else 0)
+    _check(load().hq_block_quant(
+        _raw_stream(x), _half(x, "x", batch * m * k), batch, m, k, _arg(q, "q", torch.uint8, batch * m * k),
+        _arg(sf, "sf", torch.float32, batch * (_blocks(rows) if block_2d else rows) * _blocks(cols)), flags))
+
+
+def hq_fused_swiglu_block_quant(x, q, sf, group_end=None):
+    """x [rows, 2h] = [gate | up] bfloat16 or float16 -> y = up * silu(gate)
+    quantised into q uint8 [rows, h], sf float32 [rows, ceil(h/128)] in place.
+    Rows past group_end's last value are left alone."""
+    rows, h = x.shape[0], x.shape[1] // 2
+    groups = 0 if group_end is None else group_end.numel()
+    _check(load().hq_fused_swiglu_block_quant(
+        _raw_stream(x), _half(x, "x", rows * 2 * h), rows, h, _opt(group_end, "group_end", torch.int32, groups),
+        groups, _arg(q, "q", torch.uint8, rows * h), _arg(sf, "sf", torch.float32, rows * _blocks(h)),
+        _in_flag(x)))
+
+
+def hq_block_gemm_workspace_size(m, n, k, batch=1):
+    """Bytes of workspace a dense or batched block product of this shape uses
+    on the current device (0: it never splits K)."""
+    out = ctypes.c_uint64(0)
+    _check(load().hq_block_gemm_workspace_size(0, batch, m, n, k, ctypes.byref(out)))
+    return int(out.value)
+
+
+def hq_block_gemm(a, sfa, b, sfb, out, accumulate=False, workspace=None):
+    """out[.., m, n] = a[.., m, k] b[.., n, k]^T for block-128 FP8 operands
+    (2-D, or 3-D with a batch): a uint8, sfa float32 [.., m, ceil(k/128)], b
+    uint8, sfb float32 [.., ceil(n/128), ceil(k/128)].  out is bfloat16, float16
+    or float32 (accumulate: out += the product).  With a workspace (any dtype,
+    hq_block_gemm_workspace_size bytes) the call may split K."""
+    m, k = a.shape[-2:]
+    n = b.shape[-2]
+    batch = a.shape[0] if a.dim() == 3 else 1
+    kb = _blocks(k)
+    op, flags = _out(out, batch * m * n, accumulate)
+    wp, wb = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous device tensor")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load().hq_block_gemm(
+        _raw_stream(a), flags, _arg(a, "a", torch.uint8, batch * m * k),
+        _arg(sfa, "sfa", torch.float32, batch * m * kb), _arg(b, "b", torch.uint8, batch * n * k),
+        _arg(sfb, "sfb", torch.float32, batch * _blocks(n) * kb), op, batch, m, n, k, wp, wb))
+
+
+def hq_block_group_contiguous_gemm(a, sfa, b, sfb, group_end, out, accumulate=False):
+    """Group g (rows [group_end[g-1], group_end[g]) of a) times b[g]^T; rows past
+    the last end are left alone."""
+    rows, k = a.shape
+    E, n, _ = b.shape
+    kb = _blocks(k)
+    op, flags = _out(out, rows * n, accumulate)
+    _check(load().hq_block_group_contiguous_gemm(
+        _raw_stream(a), flags, _arg(a, "a", torch.uint8, rows * k), _arg(sfa, "sfa", torch.float32, rows * kb),
+        _arg(b, "b", torch.uint8, E * n * k), _arg(sfb, "sfb", torch.float32, E * _blocks(n) * kb),
+        _arg(group_end, "group_end", torch.int32, E), E, op, rows, n, k))
+
+
+def hq_block_group_masked_gemm(a, sfa, b, sfb, masked_m, out, max_m, accumulate=False):
+    """Expert e: the first masked_m[e] rows of slot [e*max_m, (e+1)*max_m)."""
+    rows, k = a.shape
+    E, n, _ = b.shape
+    kb = _blocks(k)
+    if rows != E * max_m:
+        raise ValueError(f"a has {rows} rows, expected num_groups * max_m = {E * max_m}")
+    op, flags = _out(out, rows * n, accumulate)
+    _check(load().hq_block_group_masked_gemm(
+        _raw_stream(a), flags, _arg(a, "a", torch.uint8, rows * k), _arg(sfa, "sfa", torch.float32, rows * kb),
+        _arg(b, "b", torch.uint8, E * n * k), _arg(sfb, "sfb", torch.float32, E * _blocks(n) * kb),
+        _arg(masked_m, "masked_m", torch.int32, E), E, max_m, op, n, k))
+
+
+def hq_block_group_k_gemm(a, sfa, b, sfb, group_end, out, accumulate=False):
+    """out[g] = a[:, range g] b[:, range g]^T with range g = [group_end[g-1],
+    group_end[g]) of K: a uint8 [m, k], sfa float32 [m, k/128], b uint8 [n, k],
+    sfb float32 [ceil(n/128), k/128], out [num_groups, m, n]."""
+    m, k = a.shape
+    n = b.shape[0]
+    E = group_end.numel()
+    kb = _blocks(k)
+    op, flags = _out(out, E * m * n, accumulate)
+    _check(load().hq_block_group_k_gemm(
+        _raw_stream(a), flags, _arg(a, "a", torch.uint8, m * k), _arg(sfa, "sfa", torch.float32, m * kb),
+        _arg(b, "b", torch.uint8, n * k), _arg(sfb, "sfb", torch.float32, _blocks(n) * kb),
+        _arg(group_end, "group_end", torch.int32, E), E, op, m, n, k))
+
+
+# ---------------------------------------------------------------- token dispatch
+def moe_max_rows(tokens, topk, experts, align=1):
+    """The most rows that hq_moe_sort can use for this many pairs."""
+    pairs = tokens * topk
+    return (pairs + min(experts, pairs) * (align - 1)) // align * align
+
+
+def hq_moe_sort_workspace_size(tokens, topk, experts):
+    """Bytes of workspace hq_moe_sort needs for this shape (0: none)."""
+    out = ctypes.c_uint64(0)
+    _check(load().hq_moe_sort_workspace_size(tokens, topk, experts, ctypes.byref(out)))
+    return int(out.value)
+
+
+def hq_moe_sort(topk_ids, num_experts, align, row_map, row_pair, group_end, counts, workspace=None):
+    """(token, slot) pairs sorted by expert, in place: topk_ids int64 [T, topk]
+    -> row_map int32 [T, topk], row_pair int32 [rows], group_end and counts int32
+    [num_experts].  rows is at least moe_max_rows(...)."""
+    T, topk = topk_ids.shape
+    rows = row_pair.numel()
+    wp, wb = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous device tensor")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load().hq_moe_sort(
+        _raw_stream(topk_ids), _arg(topk_ids, "topk_ids", torch.int64, T * topk), T, topk, num_experts, align, rows,
+        _arg(row_map, "row_map", torch.int32, T * topk), _arg(row_pair, "row_pair", torch.int32, rows),
+        _arg(group_end, "group_end", torch.int32, num_experts), _arg(counts, "counts", torch.int32, num_experts),
+        wp, wb))
+
+
+def _pads(group_end, counts):
+    if (group_end is None) != (counts is None):
+        raise ValueError("group_end and counts go together")
+    E = 0 if group_end is None else group_end.numel()
+    return _opt(group_end, "group_end", torch.int32, E), _opt(counts, "counts", torch.int32, E), E
+
+
+def hq_moe_permute(x, row_map, group_end, counts, out):
+    """out[row_map[t, j]] = x[t] (rows of any dtype, whole multiples of 16 bytes),
+    and zeros in the groups' padding rows when group_end and counts are given."""
+    T, topk = row_map.shape
+    rows = out.shape[0]
+    if x.shape[0] != T or x.shape[1:] != out.shape[1:]:
+        raise ValueError("x and row_map must have the same tokens, x and out the same rows")
+    width = out[:1].numel() * out.element_size() if rows > 0 else x[:1].numel() * x.element_size()
+    ge, cn, E = _pads(group_end, counts)
+    _check(load().hq_moe_permute(
+        _raw_stream(x), _arg(x, "x", x.dtype, x.numel()), T, width, _arg(row_map, "row_map", torch.int32, T * topk),
+        topk, ge, cn, E, rows, _arg(out, "out", x.dtype, out.numel())))
+
+
+def hq_moe_permute_block_quant(x, row_map, group_end, counts, q, sf):
+    """Rows of x [T, h] (bfloat16 or float16) quantised in 1 x 128 blocks into
+    their rows of q uint8 [rows, h], sf float32 [rows, ceil(h/128)]."""
+    T, topk = row_map.shape
+    rows, h = q.shape
+    ge, cn, E = _pads(group_end, counts)
+    _check(load().hq_moe_permute_block_quant(
+        _raw_stream(x), _half(x, "x", T * h), T, h, _arg(row_map, "row_map", torch.int32, T * topk), topk, ge, cn,
+        E, rows, _arg(q, "q", torch.uint8, rows * h), _arg(sf, "sf", torch.float32, rows * _blocks(h)),
+        _in_flag(x)))
+
+
+def hq_moe_combine(y, row_map, weights, out):
+    """out[t] = sum over j of weights[t, j] y[row_map[t, j]]: y [rows, h] and out
+    [T, h] bfloat16 or float16, weights float32 [T, topk] or None (all 1: the
+    gradient of hq_moe_permute)."""
+    T, topk = row_map.shape
+    rows, h = y.shape
+    _check(load().hq_moe_combine(
+        _raw_stream(y), _half(y, "y", rows * h), T, h, _arg(row_map, "row_map", torch.int32, T * topk), topk,
+        _opt(weights, "weights", torch.float32, T * topk), rows, _half(out, "out", T * h, y), _in_flag(y)))
+
+
+def hq_moe_combine_backward(dout, y, row_map, weights, group_end, counts, dy, dweights):
+    """The gradient of hq_moe_combine: dy [rows, h] (zeros in padding rows when
+    group_end and counts are given) and dweights float32 [T, topk]."""
+    T, topk = row_map.shape
+    rows, h = y.shape
+    ge, cn, E = _pads(group_end, counts)
+    _check(load().hq_moe_combine_backward(
+        _raw_stream(y), _half(dout, "dout", T * h, y), _half(y, "y", rows * h), T, h,
+        _arg(row_map, "row_map", torch.int32, T * topk), topk, _arg(weights, "weights", torch.float32, T * topk), ge,
+        cn, E, rows, _half(dy, "dy", rows * h, y), _arg(dweights, "dweights", torch.float32, T * topk),
+        _in_flag(y)))
+
+
+def block_quantize(x, block_2d=False, transpose=False):
+    """Allocates (q, sf) with torch and runs hq_block_quant."""
+    m, k = x.shape[-2:]
+    rows, cols = (k, m) if transpose else (m, k)
+    lead = tuple(x.shape[:-2])
+    q = torch.empty(lead + (rows, cols), dtype=torch.uint8, device=x.device)
+    sf = torch.empty(lead + (_blocks(rows) if block_2d else rows, _blocks(cols)), dtype=torch.float32,
+                     device=x.device)
+    hq_block_quant(x, q, sf, block_2d, transpose)
+    return q, sf
+
+
+def moe_sort(topk_ids, num_experts, align=1):
+    """Allocates with torch and runs hq_moe_sort: (row_map, row_pair, group_end,
+    counts)."""
+    T, topk = topk_ids.shape
+    dev = topk_ids.device
+    row_map = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    row_pair = torch.empty(moe_max_rows(T, topk, num_experts, align), dtype=torch.int32, device=dev)
+    group_end = torch.empty(num_experts, dtype=torch.int32, device=dev)
+    counts = torch.empty(num_experts, dtype=torch.int32, device=dev)
+    ws = torch.empty(hq_moe_sort_workspace_size(T, topk, num_experts), dtype=torch.uint8, device=dev)
+    hq_moe_sort(topk_ids, num_experts, align, row_map, row_pair, group_end, counts, ws)
+    return row_map, row_pair, group_end, counts
 
 
 # ---------------------------------------------------------------- allocation helper

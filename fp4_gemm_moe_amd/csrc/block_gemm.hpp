@@ -1,0 +1,60 @@
+// Pieces shared by the block-128 FP8 GEMM kernels: the matrix instructions,
+// operand loads and output stores.
+#pragma once
+
+#include "block_fmt.hpp"
+#include "block_internal.hpp"
+#include "gemm_common.hpp"
+
+namespace hq {
+
+// Eight E4M3 codes -> eight FP16 values (exact: E4M3's range lies inside FP16's).
+__device__ __forceinline__ v8h decode_fp8x8(uint32_t lo, uint32_t hi) {
+  const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+  const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+  const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+  const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  return v8h{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// 16 x 16 x 128 products of E4M3 codes summed in FP32 (weights as w,
+// activations as x): lane l of the result holds rows m = l % 16, columns
+// n = 4 (l / 16) + e.  Both operands give lane group q = l / 16 the same 32 of
+// the 128 K values; which 32 they are does not matter to the sum.  The codes
+// go through FP16, whose products and sums the matrix cores keep to FP32; the
+// FP8 instructions align the eight products of a lane's dword pair to the
+// largest of them and drop what lies 14 bits below (measured: 1.5e-5 of the
+// result's norm at K = 128 against 8e-9 through FP16).
+__device__ __forceinline__ v4f dot16(v8i w, v8i x) {
+  v4f acc = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_fp8x8(w[2 * i], w[2 * i + 1]),
+                                                 decode_fp8x8(x[2 * i], x[2 * i + 1]), acc, 0, 0, 0);
+  return acc;
+}
+
+// The 16 bytes at p and the 16 at p + 64; zeros where the flag is off.
+__device__ __forceinline__ v8i load_pair(const uint8_t* p, bool in0, bool in1) {
+  uint4 u = make_uint4(0, 0, 0, 0), v = u;
+  if (in0) u = *reinterpret_cast<const uint4*>(p);
+  if (in1) v = *reinterpret_cast<const uint4*>(p + 64);
+  return v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+}
+
+// Four consecutive results at element `at` of the output.
+__device__ __forceinline__ void store4(void* out, int32_t kind, int64_t at, v4f v) {
+  if (kind == kOutBf16) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(pack_half2<false>(v[0], v[1]), pack_half2<false>(v[2], v[3]));
+  } else if (kind == kOutF16) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(pack_half2<true>(v[0], v[1]), pack_half2<true>(v[2], v[3]));
+  } else {
+    v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(out) + at);
+    if (kind == kOutF32Add) v = *o + v;
+    *o = v;
+  }
+}
+
+}  // namespace hq

@@ -1,0 +1,70 @@
+// Internal interfaces of the block-128 FP8 products and the token dispatch:
+// what their C-ABI layer (block_api.cpp) passes to the kernel translation
+// units.  Nothing here is exported.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "hq_internal.hpp"
+
+namespace hq {
+
+enum BlockOut : int32_t { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutF32Add = 3 };
+// GroupForm's forms, and the product that sums over the groups' K ranges.
+constexpr int32_t kGroupK = 3;
+
+// out[r, n] = sum over K blocks of sa[r, kb] sb[n / 128, kb] (a[r] . b[n])_kb,
+// in one of the forms of GroupForm or kGroupK.
+struct BlockGemmArgs {
+  const uint8_t* a;          // [rows, k] E4M3
+  const float* sa;           // [rows, nkb]
+  const uint8_t* b;          // [groups, n, k] E4M3 (kGroupK: [n, k])
+  const float* sb;           // [groups, nnb, nkb] (kGroupK: [nnb, nkb])
+  void* out;                 // [rows, n] (kGroupK: [groups, rows, n])
+  const int32_t* group_end;  // kContiguous: row ends; kGroupK: ends along k
+  const int32_t* counts;     // kMasked
+  int64_t rows;              // rows of a (all groups)
+  int64_t slot_rows;         // kUniform, kMasked: rows of a group
+  int64_t n, k;
+  int32_t nkb, nnb;          // ceil(k / 128), ceil(n / 128)
+  int32_t groups;
+  int32_t form;
+  int32_t out_kind;          // BlockOut
+  float* partial;            // K split: [slices, rows, n] FP32
+  int32_t slices;            // 1: unsplit
+};
+
+hipError_t launch_block_gemm(hipStream_t s, const BlockGemmArgs& args, const DeviceInfo& dev, void* workspace,
+                             uint64_t workspace_bytes);
+// Bytes of workspace that a dense or batch call of this shape uses.
+uint64_t block_gemm_workspace_bytes(const BlockGemmArgs& args, const DeviceInfo& dev);
+
+hipError_t launch_block_quant(hipStream_t s, const uint16_t* x, int64_t batch, int64_t m, int64_t k, uint8_t* q,
+                              float* sf, bool two_d, bool transpose, bool fp16);
+hipError_t launch_swiglu_block_quant(hipStream_t s, const uint16_t* x, int64_t rows, int64_t h,
+                                     const int32_t* last_end, uint8_t* q, float* sf, bool fp16);
+
+uint64_t moe_sort_workspace_bytes(int64_t pairs, int32_t experts);
+hipError_t launch_moe_sort(hipStream_t s, const int64_t* ids, int64_t pairs, int32_t experts, int32_t align,
+                           int64_t max_rows, int32_t* row_map, int32_t* row_pair, int32_t* group_end,
+                           int32_t* counts, void* workspace);
+// The rows of groups past their counts (padding): where they lie, and how
+// many there are, on the device.
+struct PadRows {
+  const int32_t* group_end;   // nullptr: no padding rows are written
+  const int32_t* counts;
+  int32_t groups;
+};
+hipError_t launch_moe_permute(hipStream_t s, const uint8_t* x, int64_t tokens, int64_t row_bytes,
+                              const int32_t* row_map, int32_t topk, PadRows pad, int64_t max_rows, uint8_t* out);
+hipError_t launch_moe_permute_block_quant(hipStream_t s, const uint16_t* x, int64_t tokens, int64_t h,
+                                          const int32_t* row_map, int32_t topk, PadRows pad, int64_t max_rows,
+                                          uint8_t* q, float* sf, bool fp16);
+hipError_t launch_moe_combine(hipStream_t s, const uint16_t* y, int64_t tokens, int64_t h, const int32_t* row_map,
+                              int32_t topk, const float* weights, int64_t max_rows, uint16_t* out, bool fp16);
+hipError_t launch_moe_combine_backward(hipStream_t s, const uint16_t* dout, const uint16_t* y, int64_t tokens,
+                                       int64_t h, const int32_t* row_map, int32_t topk, const float* weights,
+                                       PadRows pad, int64_t max_rows, uint16_t* dy, float* dweights, bool fp16);
+
+}  // namespace hq

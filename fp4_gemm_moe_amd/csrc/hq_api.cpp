@@ -12,12 +12,34 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_util.hpp"
 #include "hq.h"
 #include "hq_internal.hpp"
+
+using hq::api::aligned16;
+using hq::api::current_device;
+using hq::api::fail;
+using hq::api::kI32;
+using hq::api::launched;
+using hq::api::ok;
 
 namespace {
 
 thread_local char g_err[512] = "";
+
+// ---------------------------------------------------------------- device
+struct DevCache {
+  bool probed = false;
+  bool ok = false;
+  hq::DeviceInfo info{};
+};
+std::mutex g_dev_mu;
+DevCache g_dev[64];
+
+}  // namespace
+
+namespace hq {
+namespace api {
 
 hq_status fail(hq_status code, const char* fmt, ...) {
   va_list ap;
@@ -31,23 +53,6 @@ hq_status ok() {
   g_err[0] = '\0';
   return HQ_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-constexpr int64_t kI32 = 2147483647LL;
-
-const char* mode_name(int32_t mode) {
-  return mode == HQ_MXFP8 ? "MXFP8" : mode == HQ_MXFP4 ? "MXFP4" : mode == HQ_NVFP4 ? "NVFP4" : "?";
-}
-
-// ---------------------------------------------------------------- device
-struct DevCache {
-  bool probed = false;
-  bool ok = false;
-  hq::DeviceInfo info{};
-};
-std::mutex g_dev_mu;
-DevCache g_dev[64];
 
 hq_status current_device(hq::DeviceInfo* out) {
   int dev = -1;
@@ -79,6 +84,15 @@ hq_status current_device(hq::DeviceInfo* out) {
 hq_status launched(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(HQ_ERR_LAUNCH, "%s: launch failed: %s", what, hipGetErrorString(e));
   return ok();
+}
+
+}  // namespace api
+}  // namespace hq
+
+namespace {
+
+const char* mode_name(int32_t mode) {
+  return mode == HQ_MXFP8 ? "MXFP8" : mode == HQ_MXFP4 ? "MXFP4" : mode == HQ_NVFP4 ? "NVFP4" : "?";
 }
 
 // ---------------------------------------------------------------- scratch

@@ -452,6 +452,181 @@ hq_status hq_prefill_permute_to_masked_gemm(void* stream, const uint8_t* x, int6
                                             uint8_t* out_scale, int32_t* indice_map,
                                             int32_t* token_nums);
 
+/* ------------------------------------------------------------------------
+ * Block-128 FP8: E4M3 codes with one FP32 scale for each block of 128
+ * ------------------------------------------------------------------------
+ * Activations and gradients carry a scale per 1 x 128 block of a row, weights
+ * one per 128 x 128 block.  For a block of values x,
+ *   s = max(amax / 448, 2^-126),   code = nearest E4M3 value of x / s
+ * with IEEE FP32 divisions, ties to even, saturating at 448, the sign kept
+ * (also for zero).  A block that holds an Inf or NaN gets s = Inf or NaN and
+ * dequantises to NaN.  Scales are FP32, row-major [rows, ceil(k / 128)]
+ * (1 x 128) or [ceil(rows / 128), ceil(k / 128)] (128 x 128); the last block
+ * of a row or column may be partial.
+ */
+#define HQ_BLOCK_2D 4u      /* hq_block_quant: 128 x 128 blocks, not 1 x 128  */
+#define HQ_TRANSPOSE 8u     /* hq_block_quant: codes and scales of x^T        */
+#define HQ_OUT_FP32 0x200u  /* products: out holds FP32                       */
+#define HQ_ACCUMULATE 0x400u /* products, with HQ_OUT_FP32: out += the product */
+
+/*
+ * Block quantisation of BF16 (FP16 with HQ_IN_FP16) tensors.
+ *   x [batch, m, k];  q [batch, m, k] codes, sf [batch, m, ceil(k/128)]
+ * With HQ_TRANSPOSE the tensor quantised is x^T per batch item: q
+ * [batch, k, m], sf [batch, k, ceil(m/128)] (m % 32 == 0) -- the operand of a
+ * product that sums over x's rows, or weights for a gradient with respect to
+ * activations.  With HQ_BLOCK_2D the blocks are 128 x 128: sf
+ * [batch, ceil(rows/128), ceil(cols/128)] of q's rows and columns.
+ *   k % 32 == 0; 0 <= batch <= 65535; x, q 16-byte aligned, sf 4-byte aligned.
+ */
+hq_status hq_block_quant(void* stream, const uint16_t* x, int64_t batch, int64_t m,
+                         int64_t k, uint8_t* q, float* sf, uint32_t flags);
+
+/*
+ * SwiGLU with block quantisation of the result: x [rows, 2h] = [gate | up]
+ * (BF16, FP16 with HQ_IN_FP16), y = up * gate / (1 + exp(-gate)) in FP32, then
+ * q [rows, h], sf [rows, ceil(h/128)] as hq_block_quant in 1 x 128 blocks.
+ * group_end (optional, device int32 [num_groups]): rows at or past its last
+ * value are neither read nor written.  h % 32 == 0.
+ */
+hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t rows,
+                                      int64_t h, const int32_t* group_end,
+                                      int32_t num_groups, uint8_t* q, float* sf,
+                                      uint32_t flags);
+
+/*
+ * Block-128 FP8 products.  With K blocks kb of 128,
+ *   out[r, n] = sum over kb of sfa[r, kb] sfb[n / 128, kb]
+ *               * sum over k in kb of a[r, k] b[n, k]
+ * the inner sums on the matrix cores and the outer one in FP32, rounded once
+ * to BF16 (FP16 with HQ_OUT_FP16; kept in FP32 with HQ_OUT_FP32; added in
+ * FP32 to out with HQ_OUT_FP32 | HQ_ACCUMULATE).  A product of two scales
+ * has to be a finite FP32 number.
+ *   a [.., k] codes, sfa [.., ceil(k/128)] (1 x 128 blocks);
+ *   b [.., n, k] codes, sfb [.., ceil(n/128), ceil(k/128)] (128 x 128 blocks).
+ * k % 32 == 0, n % 8 == 0, 256 k < 2^31; a, b, out and the workspace 16-byte
+ * aligned, scales 4-byte aligned.  m == 0 or n == 0 is a no-op.
+ * Gradients: with W [n, k] and dY [m, n], the gradient for X [m, k] is the
+ * product of dY's row codes with W's HQ_BLOCK_2D | HQ_TRANSPOSE codes, and the
+ * gradient for W that of dY's HQ_TRANSPOSE codes with X's
+ * HQ_BLOCK_2D | HQ_TRANSPOSE codes (hq_block_group_k_gemm per expert).
+ *
+ * hq_block_gemm: dense (batch 1) or batched; a [batch, m, k], b [batch, n, k],
+ * out [batch, m, n].  hq_block_gemm_workspace_size gives the bytes of FP32
+ * workspace that this shape uses when it splits K (0: never); with a smaller
+ * or no workspace the call runs unsplit.  No call uses more than
+ * HQ_BLOCK_WORKSPACE_BYTES.  Two calls in flight need two workspaces.
+ */
+#define HQ_BLOCK_WORKSPACE_BYTES (64u << 20)
+hq_status hq_block_gemm(void* stream, uint32_t flags, const uint8_t* a, const float* sfa,
+                        const uint8_t* b, const float* sfb, void* out, int64_t batch,
+                        int64_t m, int64_t n, int64_t k, void* workspace,
+                        uint64_t workspace_bytes);
+hq_status hq_block_gemm_workspace_size(uint32_t flags, int64_t batch, int64_t m,
+                                       int64_t n, int64_t k, uint64_t* bytes);
+
+/* Per expert over contiguous rows: as hq_group_contiguous_gemm (device
+ * group_end [num_groups], clamped to non-decreasing ends in [0, m_total]; rows
+ * at or past the last end are not written); b [num_groups, n, k], sfb
+ * [num_groups, ceil(n/128), ceil(k/128)]. */
+hq_status hq_block_group_contiguous_gemm(void* stream, uint32_t flags, const uint8_t* a,
+                                         const float* sfa, const uint8_t* b,
+                                         const float* sfb, const int32_t* group_end,
+                                         int32_t num_groups, void* out, int64_t m_total,
+                                         int64_t n, int64_t k);
+
+/* Per expert over padded slots: as hq_group_masked_gemm (device masked_m
+ * [num_groups], clamped to [0, max_m_per_group]; only valid rows are written). */
+hq_status hq_block_group_masked_gemm(void* stream, uint32_t flags, const uint8_t* a,
+                                     const float* sfa, const uint8_t* b,
+                                     const float* sfb, const int32_t* masked_m,
+                                     int32_t num_groups, int64_t max_m_per_group,
+                                     void* out, int64_t n, int64_t k);
+
+/* Per expert over a range of K: group g sums k in [group_end[g-1],
+ * group_end[g]) of a [m, k_total], sfa [m, k_total/128], b [n, k_total], sfb
+ * [ceil(n/128), k_total/128] into out [num_groups, m, n] -- the weights'
+ * gradient of a grouped-contiguous product.  group_end (device, multiples of
+ * 128 as hq_moe_sort with align 128 gives; others are rounded down) is clamped
+ * to non-decreasing ends in [0, k_total]; an empty range gives zeros (leaves
+ * out as it is with HQ_ACCUMULATE).  k_total % 128 == 0. */
+hq_status hq_block_group_k_gemm(void* stream, uint32_t flags, const uint8_t* a,
+                                const float* sfa, const uint8_t* b, const float* sfb,
+                                const int32_t* group_end, int32_t num_groups, void* out,
+                                int64_t m, int64_t n, int64_t k_total);
+
+/* ------------------------------------------------------------------------
+ * Tokens sorted by expert, and back
+ * ------------------------------------------------------------------------
+ * Pair i = t * topk + j is slot j of token t; ids outside [0, num_experts)
+ * are unassigned.  Expert g's rows start at the end of expert g - 1 (0 for the
+ * first); its pairs take consecutive rows in the order of i; its end is its
+ * start plus its count rounded up to a multiple of align.  The result does not
+ * vary from run to run.
+ *   topk_ids  int64 [num_tokens, topk], 1 <= topk <= 64
+ *   row_map   int32 [num_tokens, topk]: the pair's row, -1 if unassigned
+ *   row_pair  int32 [max_rows]: the row's pair i, -1 where it has none
+ *   group_end, counts  int32 [num_experts]: padded ends, pairs per expert
+ * max_rows is at least the most rows that any ids can take,
+ * (P + min(num_experts, P) (align - 1)) / align * align for P = num_tokens *
+ * topk (HQ_ERR_SHAPE otherwise).  1 <= num_experts, align <= 1024.  The
+ * workspace (4-byte aligned) holds hq_moe_sort_workspace_size bytes, never
+ * more than HQ_SORT_WORKSPACE_BYTES; it may be NULL where that is 0.
+ */
+#define HQ_SORT_WORKSPACE_BYTES (1u << 20)
+hq_status hq_moe_sort(void* stream, const int64_t* topk_ids, int64_t num_tokens,
+                      int32_t topk, int32_t num_experts, int32_t align, int64_t max_rows,
+                      int32_t* row_map, int32_t* row_pair, int32_t* group_end,
+                      int32_t* counts, void* workspace, uint64_t workspace_bytes);
+hq_status hq_moe_sort_workspace_size(int64_t num_tokens, int32_t topk,
+                                     int32_t num_experts, uint64_t* bytes);
+
+/*
+ * The calls below walk a row_map as hq_moe_sort writes it.  Entries outside
+ * [0, max_rows) count as unassigned; no row may occur twice.  With group_end
+ * and counts (both or neither) the padding rows, those of a group past its
+ * count, are written as zeros (scales 2^-126), as a product over K ranges
+ * needs them; other rows are not written.  Values are BF16 (FP16 with
+ * HQ_IN_FP16, for every 16-bit tensor of the call).
+ *
+ * hq_moe_permute: out[row_map[t, j]] = x[t], rows of row_bytes bytes (a
+ * multiple of 16), copied bit for bit.  Its gradient is hq_moe_combine with
+ * weights NULL.
+ * hq_moe_permute_block_quant: the same with the row quantised in 1 x 128
+ * blocks: q [max_rows, hidden], sf [max_rows, ceil(hidden/128)];
+ * hidden % 32 == 0.
+ */
+hq_status hq_moe_permute(void* stream, const uint8_t* x, int64_t num_tokens,
+                         int64_t row_bytes, const int32_t* row_map, int32_t topk,
+                         const int32_t* group_end, const int32_t* counts,
+                         int32_t num_groups, int64_t max_rows, uint8_t* out);
+hq_status hq_moe_permute_block_quant(void* stream, const uint16_t* x, int64_t num_tokens,
+                                     int64_t hidden, const int32_t* row_map, int32_t topk,
+                                     const int32_t* group_end, const int32_t* counts,
+                                     int32_t num_groups, int64_t max_rows, uint8_t* q,
+                                     float* sf, uint32_t flags);
+
+/*
+ * hq_moe_combine: out[t] = sum over assigned j of weights[t, j]
+ * y[row_map[t, j]] (weights FP32; NULL: 1), summed in FP32 in the order of j,
+ * rounded once; a token without a row gets zeros.  hidden % 8 == 0.
+ * hq_moe_combine_backward, for the gradient dout of out:
+ *   dy[row_map[t, j]] = weights[t, j] dout[t]
+ *   dweights[t, j]    = sum over h of dout[t, h] y[row_map[t, j], h]   (FP32;
+ *                       0 if unassigned)
+ */
+hq_status hq_moe_combine(void* stream, const uint16_t* y, int64_t num_tokens,
+                         int64_t hidden, const int32_t* row_map, int32_t topk,
+                         const float* weights, int64_t max_rows, uint16_t* out,
+                         uint32_t flags);
+hq_status hq_moe_combine_backward(void* stream, const uint16_t* dout, const uint16_t* y,
+                                  int64_t num_tokens, int64_t hidden,
+                                  const int32_t* row_map, int32_t topk,
+                                  const float* weights, const int32_t* group_end,
+                                  const int32_t* counts, int32_t num_groups,
+                                  int64_t max_rows, uint16_t* dy, float* dweights,
+                                  uint32_t flags);
+
 #ifdef __cplusplus
 }
 #endif
