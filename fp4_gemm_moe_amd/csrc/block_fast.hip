@@ -1,0 +1,17 @@
+// Instantiations of the tiled block-128 FP8 GEMM on the FP8 matrix
+// instructions: BF16 results, and FP32 partial sums of a K split that a BF16
+// result is made of.
+#include "block_launch.hpp"
+
+namespace hq {
+
+hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, bool nt) {
+  using namespace blk;
+  switch (tile) {
+    case kTile256x256: return launch_out<Cfg<256, 256, 2, 4, 2, true>, kOutBf16, kOutF32>(s, p, dev, nt);
+    case kTile128x128: return launch_out<Cfg<128, 128, 2, 2, 4, true>, kOutBf16, kOutF32>(s, p, dev, nt);
+    default: return launch_out<Cfg<64, 128, 2, 2, 5, true>, kOutBf16, kOutF32>(s, p, dev, nt);
+  }
+}
+
+}  // namespace hq

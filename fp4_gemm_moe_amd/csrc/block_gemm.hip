@@ -8,7 +8,8 @@
 // step from zero, and the vector unit adds that sum times sa sb to the FP32
 // accumulator.  The scales are per row of a and per 128 columns, so a lane's
 // factor is one product for all accumulators of its row.
-#include "block_gemm.hpp"
+#include "block_launch.hpp"
+#include "hq.h"
 
 namespace hq {
 namespace {
@@ -112,17 +113,88 @@ __global__ __launch_bounds__(W * 64) void block_gemm_direct(BlockGemmArgs p) {
   }
 }
 
+// ------------------------------------------------------------------ K split
+// out = the slices' FP32 partial sums, added in slice order.
+constexpr int kReduceThreads = 256;
+__global__ __launch_bounds__(kReduceThreads) void block_reduce(const float* __restrict__ partial, int slices,
+                                                               int64_t quads, void* out, int32_t kind) {
+  const int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x;
+  if (i >= quads) return;
+  const v4f* src = reinterpret_cast<const v4f*>(partial) + i;
+  v4f v = src[0];
+  for (int s = 1; s < slices; ++s) v += src[s * quads];
+  store4(out, kind, 4 * i, v);
+}
+
+bool fast_path(const BlockGemmArgs& p) { return p.out_kind == kOutBf16 && p.nkb >= 4; }
+
+struct Plan {
+  bool direct;
+  int tile;
+  int slices;
+  uint64_t bytes;      // workspace of the split
+};
+
+Plan plan_gemm(const BlockGemmArgs& p, const DeviceInfo& dev) {
+  Plan pl{false, kTile256x256, 1, 0};
+  const bool fast = fast_path(p);
+  const int64_t per = p.form == kContiguous ? (p.rows + p.groups - 1) / p.groups
+                                            : (p.form == kGroupK ? p.rows : p.slot_rows);
+  if (p.form == kUniform && p.slot_rows <= 16) {
+    pl.direct = true;
+    return pl;
+  }
+  int bm = 256, bn = 256;
+  if (per <= 64 || p.nkb < 4) {        // the larger tiles fetch four K blocks' scales at a time
+    pl.tile = kTile64x128;
+    bm = 64, bn = 128;
+  } else if (fast && per <= 128) {
+    pl.tile = kTile128x128;
+    bm = 128, bn = 128;
+  } else if (!fast) {
+    pl.tile = kTile256x128;
+    bn = 128;
+  }
+  if (p.form == kUniform) {
+    const int64_t tiles = (p.slot_rows + bm - 1) / bm * p.groups * ((p.n + bn - 1) / bn);
+    int64_t s = dev.num_cus / tiles;
+    if (s > p.nkb / 4) s = p.nkb / 4;
+    const int64_t most = (int64_t)(HQ_BLOCK_WORKSPACE_BYTES / 4) / (p.rows * p.n);
+    if (s > most) s = most;
+    if (s > 1) {
+      pl.slices = (int)s;
+      pl.bytes = (uint64_t)s * p.rows * p.n * 4;
+    }
+  }
+  return pl;
+}
+
 }  // namespace
 
-uint64_t block_gemm_workspace_bytes(const BlockGemmArgs&, const DeviceInfo&) { return 0; }
+uint64_t block_gemm_workspace_bytes(const BlockGemmArgs& p, const DeviceInfo& dev) { return plan_gemm(p, dev).bytes; }
 
-hipError_t launch_block_gemm(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo&, void*, uint64_t) {
-  constexpr int MF = 2, NF = 2, W = 4;
-  int64_t per = p.form == kContiguous ? (p.rows + p.groups - 1) / p.groups : (p.form == kGroupK ? p.rows : p.slot_rows);
-  int64_t z = (per + 16 * MF - 1) / (16 * MF);
-  z = z < 1 ? 1 : (z > 65535 ? 65535 : z);
-  const dim3 grid((unsigned)((p.n + 16 * NF - 1) / (16 * NF)), (unsigned)p.groups, (unsigned)z);
-  hipLaunchKernelGGL((block_gemm_direct<MF, NF, W>), grid, dim3(W * 64), 0, s, p);
+hipError_t launch_block_gemm(hipStream_t s, const BlockGemmArgs& args, const DeviceInfo& dev, void* workspace,
+                             uint64_t workspace_bytes) {
+  const Plan pl = plan_gemm(args, dev);
+  BlockGemmArgs p = args;
+  if (pl.direct) {
+    constexpr int MF = 1, NF = 1, W = 8;
+    const dim3 grid((unsigned)((p.n + 16 * NF - 1) / (16 * NF)), (unsigned)p.groups, 1);
+    hipLaunchKernelGGL((block_gemm_direct<MF, NF, W>), grid, dim3(W * 64), 0, s, p);
+    return hipGetLastError();
+  }
+  const bool nt = p.form == kMasked && p.slot_rows <= 256;
+  const bool split = pl.slices > 1 && workspace_bytes >= pl.bytes;
+  if (split) {
+    p.slices = pl.slices;
+    p.out = workspace;
+    p.out_kind = kOutF32;
+  }
+  hipError_t e = fast_path(args) ? launch_block_fast(s, p, dev, pl.tile, nt) : launch_block_exact(s, p, dev, pl.tile, nt);
+  if (e != hipSuccess || !split) return e;
+  const int64_t quads = p.rows * p.n / 4;
+  hipLaunchKernelGGL(block_reduce, dim3((unsigned)((quads + kReduceThreads - 1) / kReduceThreads)), dim3(kReduceThreads),
+                     0, s, static_cast<const float*>(workspace), pl.slices, quads, args.out, args.out_kind);
   return hipGetLastError();
 }
 

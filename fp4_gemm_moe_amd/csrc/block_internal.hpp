@@ -31,8 +31,7 @@ struct BlockGemmArgs {
   int32_t groups;
   int32_t form;
   int32_t out_kind;          // BlockOut
-  float* partial;            // K split: [slices, rows, n] FP32
-  int32_t slices;            // 1: unsplit
+  int32_t slices;            // kUniform: K slices; out then holds [slices, rows, n] FP32 partial sums
 };
 
 hipError_t launch_block_gemm(hipStream_t s, const BlockGemmArgs& args, const DeviceInfo& dev, void* workspace,
