@@ -29,8 +29,6 @@
 namespace hq {
 namespace blk {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
-
 __device__ __forceinline__ uint32_t ufirst(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t ufirst64(int64_t v) {
   const uint64_t u = (uint64_t)v;
@@ -89,7 +87,7 @@ struct Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
   static constexpr bool FAST = FAST_;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
-  static constexpr int WTM = BM / WM, WTN = BN / WN, FI = WTM / 32, FJ = WTN / 32;
+  static constexpr int WTM = BM / WM, WTN = BN / WN, FI = WTM / 16, FJ = WTN / 16;
   static constexpr int AL = BM / 8 / WAVES, BL = BN / 8 / WAVES;   // 16-byte loads a thread, per step
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int NB = BN / 128;
@@ -102,7 +100,7 @@ struct Cfg {
   static constexpr int SBUFS = GROUPED ? 2 : ST;
   static constexpr int SMEM = ST * STAGE + SBUFS * SBUF;
   static constexpr int SW = BM / 64;              // waves that load A's scales; wave SW loads B's
-  static_assert(WTM % 32 == 0 && WTN % 32 == 0 && 128 % WTN == 0 && BN % 128 == 0, "wave tiles");
+  static_assert(WTM % 32 == 0 && WTN == 64 && BN % 128 == 0, "wave tiles");
   static_assert(AL >= 1 && BL >= 1 && BM / 8 % WAVES == 0 && BN / 8 % WAVES == 0, "whole loads");
   static_assert(BM % 64 == 0 && SW + 1 <= WAVES, "scale loads");
 };
@@ -123,6 +121,14 @@ struct Operands {
   const float *sa, *sb;
   uint32_t a_bytes, b_bytes, sa_bytes, sb_bytes;
 };
+
+// The next tiles of a workgroup, by round, kept in LDS: the loads look them up
+// in the middle of a K loop, where there are no registers to work them out.
+struct Upcoming {
+  Tile t;
+  Operands o;
+};
+constexpr int kRing = 8;
 
 // Tiles are numbered in blocks of 8 m-tiles x all n-tiles, n-major inside a
 // block, so that the tiles an XCD's workgroups run side by side share operand
@@ -245,11 +251,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   constexpr int FI = C::FI, FJ = C::FJ, ST = C::ST, AL = C::AL, BL = C::BL;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ Table table;
+  __shared__ Upcoming ring[kRing];
   const Order ord = make_order<C>(p, table);
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = (int)ufirst((uint32_t)(tid >> 6));
   const int wm = w / C::WN, wn = w % C::WN;
-  const int h = lane >> 5, r32 = lane & 31;
 
   // XCD-aware order: workgroup b runs on XCD b % 8.  A launch over one plane
   // of uniform tiles gives each XCD a contiguous eighth of them; other forms
@@ -288,13 +294,62 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   const uint32_t hop = (uint32_t)p.k * (C::WAVES * 8);      // bytes from one load's rows to the next one's
   const uint32_t lds0 = ufirst((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)smem);
 
+  // Every wave writes the same values and reads its own; it runs at most a
+  // step ahead of the others, so a slot is not reused while it is needed.
+  auto plan = [&](int round) {
+    Upcoming u;
+    const int id = tile_at(round);
+    if (id < last) {
+      u.t = make_tile<C>(p, table, ord, id);
+      u.o = operands<C>(p, u.t);
+    } else {                 // nothing left: steps load zeros from empty descriptors
+      u.t = Tile{};
+      u.t.nk = 0x7FFFFFFF;
+      u.o = Operands{};
+    }
+    if (lane == 0) ring[round % kRing] = u;
+  };
+  static_assert(ST + 2 <= kRing, "tiles in flight");
+#pragma unroll 1
+  for (int r = 0; r < ST; ++r) plan(r);
+  auto upcoming = [&](int round) -> Operands {
+    const Operands& v = ring[round % kRing].o;
+    Operands o;
+    o.a = uniform(v.a);
+    o.b = uniform(v.b);
+    o.sa = uniform(v.sa);
+    o.sb = uniform(v.sb);
+    o.a_bytes = ufirst(v.a_bytes);
+    o.b_bytes = ufirst(v.b_bytes);
+    o.sa_bytes = ufirst(v.sa_bytes);
+    o.sb_bytes = ufirst(v.sb_bytes);
+    return o;
+  };
+  auto tile_of = [&](int round) -> Tile {
+    const Tile& v = ring[round % kRing].t;
+    Tile t;
+    t.g = (int)ufirst((uint32_t)v.g);
+    t.slice = (int)ufirst((uint32_t)v.slice);
+    t.nk = (int)ufirst((uint32_t)v.nk);
+    t.kb0 = (int)ufirst((uint32_t)v.kb0);
+    t.row0 = ufirst64(v.row0);
+    t.row_end = ufirst64(v.row_end);
+    t.n0 = ufirst64(v.n0);
+    return t;
+  };
+
   // ---------------------------------------------------------------- loads
   int lround = 0, lk = 0, lstep = 0, lgroup = 0;   // load cursor: tile round, step in it, stage, scale buffer
-  Tile lt = make_tile<C>(p, table, ord, tile_at(0));
-  Operands lo = operands<C>(p, lt);
+  int lkb0, lnk;                                   // that tile's first K block and its steps
+  Operands lo = upcoming(0);
+  {
+    const Tile t = tile_of(0);
+    lkb0 = t.kb0;
+    lnk = t.nk;
+  }
   // issues part `part` of `parts` of the cursor's step; bit 31 of an offset drops the load
   auto issue = [&](int part, int parts) {
-    const int kb = lt.kb0 + lk;
+    const int kb = lkb0 + lk;
     const uint32_t st = lds0 + (uint32_t)lstep * C::STAGE + (uint32_t)w * 1024;
     const uint32_t ko = (uint32_t)kb * 128;
     const uint32_t d = kb == p.nkb - 1 ? drop : 0u;
@@ -317,7 +372,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   // Scales: waves 0 .. SW - 1 bring 64 rows of A each, wave SW the B blocks'.
   auto issue_scales = [&]() {
     if (w > C::SW || (C::GROUPED && (lk & 3) != 0)) return;
-    const int kb = lt.kb0 + lk;
+    const int kb = lkb0 + lk;
     const bool isb = w == C::SW;
     const __amdgpu_buffer_rsrc_t r = isb ? rsrc(lo.sb, lo.sb_bytes) : rsrc(lo.sa, lo.sa_bytes);
     const uint32_t row = isb ? lane : w * 64 + lane;
@@ -332,18 +387,13 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     lstep = lstep + 1 == ST ? 0 : lstep + 1;
     ++lk;
     if (C::GROUPED && (lk & 3) == 0) lgroup ^= 1;
-    if (lk >= lt.nk) {
+    if (lk >= lnk) {
       if (C::GROUPED && (lk & 3) != 0) lgroup ^= 1;
       lk = 0;
       ++lround;
-      const int id = tile_at(lround);
-      if (id < last) {
-        lt = make_tile<C>(p, table, ord, id);
-        lo = operands<C>(p, lt);
-      } else {                 // nothing left: the remaining steps load zeros from empty descriptors
-        lt.nk = 0x7FFFFFFF;
-        lo.a_bytes = lo.b_bytes = lo.sa_bytes = lo.sb_bytes = 0;
-      }
+      lo = upcoming(lround);
+      lkb0 = (int)ufirst((uint32_t)ring[lround % kRing].t.kb0);
+      lnk = (int)ufirst((uint32_t)ring[lround % kRing].t.nk);
     }
   };
   auto issue_all = [&]() {
@@ -371,209 +421,258 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   land();
 
   // ---------------------------------------------------------------- compute
-  // Fragment reads: fragment row i of a wave tile starts at LDS row 32 i of
-  // the wave's rows; its swizzle is that of fragment row 0 ^ 4 (i & 1).
-  // xa / xb[e]: the byte offset of logical chunk 2 e + h in an i = 0 row of A / B.
-  uint32_t xa[4], xb[4];
-  {
-    const int sa0 = swz(((wm * C::WTM) & 63) + r32), sb0 = swz(((wn * C::WTN) & 63) + r32);
+  // Fragments of 16 rows: lane l holds row l % 16, chunks q and 4 + q (q = l /
+  // 16) of its 128 codes.  A's fragment i starts at the wave's LDS row 16 i.
+  // B's fragments come in pairs over 32 columns, interleaved by fours, so that
+  // the accumulators of a pair are eight neighbouring columns of a lane:
+  // row x of fragment j is column 32 (j / 2) + 8 (x / 4) + 4 (j % 2) + x % 4.
+  const int x16 = lane & 15, q = lane >> 4;
+  uint32_t xa[2], xb[2];       // byte offsets of chunk q of fragments 0 and 1
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      xa[e] = (uint32_t)(r32 * 128 + (((2 * e + h) ^ sa0) << 4));
-      xb[e] = (uint32_t)(r32 * 128 + (((2 * e + h) ^ sb0) << 4));
-    }
+  for (int e = 0; e < 2; ++e) {
+    const int ra = 16 * e + x16, rb = 8 * (x16 >> 2) + 4 * e + (x16 & 3);
+    xa[e] = (uint32_t)(ra * 128 + ((q ^ swz(wm * C::WTM + ra)) << 4));
+    xb[e] = (uint32_t)(rb * 128 + ((q ^ swz(wn * C::WTN + rb)) << 4));
   }
-  struct Raw {
-    uint4 c[4];      // the lane's 64 codes of its row's 128
-  };
-  auto rd = [&](const uint8_t* base, const uint32_t (&xo)[4], int i) -> Raw {
-    Raw f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      f.c[e] = *reinterpret_cast<const uint4*>(base + i * 4096 + xo[e ^ (2 * (i & 1))]);
-    return f;
-  };
-  auto pair = [](const uint4& u, const uint4& v) -> v8i {
-    return v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+  // A fragment's 32 codes of a lane; whole vectors throughout, so that they
+  // stay in consecutive registers across the loop.
+  // fragment i: 16 i rows on, i / 2 flips the swizzle's bit 2 every 32 rows; chunk 4 + q is bit 2's other value
+  auto rd = [&](const uint8_t* base, const uint32_t (&xo)[2], int i) -> v8i {
+    const uint32_t o = xo[i & 1], flip = ((i >> 1) & 1) * 64u;
+    const uint8_t* r = base + (i >> 1) * 4096;
+    const v4i lo4 = *reinterpret_cast<const v4i*>(r + (o ^ flip));
+    const v4i hi4 = *reinterpret_cast<const v4i*>(r + (o ^ flip ^ 64u));
+    return __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  v16f acc[FI][FJ];
+  // Steps overlap: the last fragment row of a step multiplies after the barrier
+  // that ends it (head), while the next step's first fragments are read into the
+  // registers that it frees; the other rows (body) follow, with the loads.  So
+  // the matrix cores have work while the first reads of a step are under way,
+  // and every fragment of a step has been read when the barrier frees its stage.
+  v4f acc[FI][FJ];
   int stage = 0, group = 0;
-  // One step of tile t on stage `stage`; `k` is its place in the tile.
-  constexpr int G = FI * FJ;
-  auto step = [&](const Tile& t, int k) {
+  constexpr int G = FI * FJ, GB = G - FJ;     // fragments of a step, of its body
+  constexpr int LS = GB < AL + BL ? GB : AL + BL;     // load slots, from the body's first fragment on
+  auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
+  constexpr int D = C::FAST ? 1 : 2;
+  v4f tm[D][FJ];                // FAST: fragment g's sum, added up two fragments later; else a row's, added during the next
+  float f[FI], flast = 0.0f;    // the step's factors; the last row's, of the step before
+  v8i ra[2];                    // A's fragments of this row and the next
+  v8i rb[FJ];                   // B's
+  v8h da[C::FAST ? 1 : 2][4], db[C::FAST ? 1 : FJ][4];     // widened
+  auto add = [&](int i, int j, float fi) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[i][j][r] = __builtin_fmaf(tm[C::FAST ? 0 : i & 1][j][r], fi, acc[i][j][r]);
+  };
+  auto widen1 = [](const v8i& r, int e) -> v8h { return decode_fp8x8((uint32_t)r[2 * e], (uint32_t)r[2 * e + 1]); };
+  const uint32_t wa = wm * C::WTM * 128, wb = C::BM * 128 + wn * C::WTN * 128;
+  // the first fragments of the current stage's step
+  auto read_first = [&]() {
     const uint8_t* base = smem + stage * C::STAGE;
-    const uint8_t* la = base + wm * C::WTM * 128;
-    const uint8_t* lb = base + C::BM * 128 + wn * C::WTN * 128;
-    // scale factors
-    float f[FI];
-    {
-      const int row = wm * C::WTM + r32, nb = wn * C::WTN / 128;
-      const uint8_t* s = smem + ST * C::STAGE;
-      float sbv;
-      if constexpr (C::GROUPED) {
-        const int kb = t.kb0 + k, g0 = t.kb0 + (k & ~3);
-        s += group * C::SBUF + (kb - (g0 < p.nkb - 4 ? g0 : p.nkb - 4)) * 4;
-        sbv = *reinterpret_cast<const float*>(s + C::BM * 16 + nb * 16);
+    ra[0] = rd(base + wa, xa, 0);
 #pragma unroll
-        for (int i = 0; i < FI; ++i) f[i] = *reinterpret_cast<const float*>(s + (row + 32 * i) * 16) * sbv;
-      } else {
-        s += stage * C::SBUF;
-        sbv = *reinterpret_cast<const float*>(s + C::BM * 4 + nb * 4);
+    for (int j = 0; j < FJ; ++j) rb[j] = rd(base + wb, xb, j);
+    if constexpr (!C::FAST) {
 #pragma unroll
-        for (int i = 0; i < FI; ++i) f[i] = *reinterpret_cast<const float*>(s + (row + 32 * i) * 4) * sbv;
+      for (int e = 0; e < 4; ++e) {
+        da[0][e] = widen1(ra[0], e);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) db[j][e] = widen1(rb[j], e);
       }
     }
-    if (t.nk == 0) {           // an empty K range: the codes read as zeros, the scales as anything
+  };
+  // the factors of place k of tile t
+  auto read_f = [&](const Tile& t, int k) {
+    const int row = wm * C::WTM + x16, nb = wn * C::WTN / 128;
+    const uint8_t* s = smem + ST * C::STAGE;
+    float sbv, v[FI];
+    if constexpr (C::GROUPED) {
+      const int kb = t.kb0 + k, g0 = t.kb0 + (k & ~3);
+      s += group * C::SBUF + (kb - (g0 < p.nkb - 4 ? g0 : p.nkb - 4)) * 4;
+      sbv = *reinterpret_cast<const float*>(s + C::BM * 16 + nb * 16);
 #pragma unroll
-      for (int i = 0; i < FI; ++i) f[i] = 0.0f;
-    }
-    auto add = [&](int i, int j, const v16f& t16) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        acc[i][j][r] = __builtin_fmaf(t16[r], f[i], acc[i][j][r]);
-    };
-    v16f tm[2];
-    Raw ra = rd(la, xa, 0);
-    if constexpr (C::FAST) {
-      Raw rb[FJ];
-#pragma unroll
-      for (int j = 0; j < FJ; ++j) rb[j] = rd(lb, xb, j);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < FI; ++i) {
-#pragma unroll
-        for (int j = 0; j < FJ; ++j) {
-          const int g = i * FJ + j;
-          v16f tt = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pair(rb[j].c[0], rb[j].c[1]), pair(ra.c[0], ra.c[1]),
-                                                                    v16f{}, 0, 0, 0, 0, 0, 0);
-          tm[g & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pair(rb[j].c[2], rb[j].c[3]),
-                                                                      pair(ra.c[2], ra.c[3]), tt, 0, 0, 0, 0, 0, 0);
-          issue(g, G);
-          // the next row's fragment lands under this group's matrix instructions
-          if (j == FJ - 1 && i + 1 < FI) ra = rd(la, xa, i + 1);
-          __builtin_amdgcn_sched_barrier(0);
-          if (g > 0) add((g - 1) / FJ, (g - 1) % FJ, tm[(g - 1) & 1]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+      for (int i = 0; i < FI; ++i) v[i] = *reinterpret_cast<const float*>(s + (row + 16 * i) * 16);
     } else {
-      v8h db[FJ][8];
+      s += stage * C::SBUF;
+      sbv = *reinterpret_cast<const float*>(s + C::BM * 4 + nb * 4);
+#pragma unroll
+      for (int i = 0; i < FI; ++i) v[i] = *reinterpret_cast<const float*>(s + (row + 16 * i) * 4);
+    }
+    // an empty K range: the codes read as zeros, the scales as anything
+    const bool any = t.nk != 0;
+#pragma unroll
+    for (int i = 0; i < FI; ++i) f[i] = any ? v[i] * sbv : 0.0f;
+  };
+  // Row i of the step whose fragments are in registers.  next: base of the row
+  // read for after it (row 0 of the next step for the last row, whose B
+  // fragments are replaced too).
+  auto row = [&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    constexpr bool kHead = i == FI - 1;
+    const uint8_t* base = smem + stage * C::STAGE;
+    if constexpr (C::FAST) {
+      ra[(i + 1) & 1] = rd(base + wa, xa, kHead ? 0 : i + 1);
 #pragma unroll
       for (int j = 0; j < FJ; ++j) {
-        const Raw rb = rd(lb, xb, j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          db[j][2 * e] = decode_fp8x8(rb.c[e].x, rb.c[e].y);
-          db[j][2 * e + 1] = decode_fp8x8(rb.c[e].z, rb.c[e].w);
-        }
+        constexpr int kBack = 2;       // added up this many fragments later
+        const int g = i * FJ + j;
+        tm[0][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rb[j], ra[i & 1], v4f{}, 0, 0, 0, 0, 0, 0);
+        if (!kHead && g < LS) issue(g, LS);
+        fence();
+        if constexpr (kHead) rb[j] = rd(base + wb, xb, j);
+        if (g >= kBack) add((g - kBack) / FJ, (g - kBack) % FJ, f[(g - kBack) / FJ]);
+        else add(FI - 1, FJ - kBack + g, flast);
+        fence();
       }
+    } else {
+      ra[0] = rd(base + wa, xa, kHead ? 0 : i + 1);
+      if constexpr (kHead) {
 #pragma unroll
-      for (int i = 0; i < FI; ++i) {
-        v8h da[8];
+        for (int j = 0; j < FJ; ++j) rb[j] = rd(base + wb, xb, j);
+      }
+      fence();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          da[2 * e] = decode_fp8x8(ra.c[e].x, ra.c[e].y);
-          da[2 * e + 1] = decode_fp8x8(ra.c[e].z, ra.c[e].w);
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+          tm[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(db[j][e], da[i & 1][e], e == 0 ? v4f{} : tm[i & 1][j],
+                                                                0, 0, 0);
+        if (!kHead && i * FJ + e < LS) issue(i * FJ + e, LS);
+        if (i > 0) add(i > 0 ? i - 1 : 0, e, f[i > 0 ? i - 1 : 0]);
+        else add(FI - 1, e, flast);
+        if (e > 0) {
+          da[(i + 1) & 1][e - 1] = widen1(ra[0], e - 1);
+          if constexpr (kHead) {
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) db[j][e - 1] = widen1(rb[j], e - 1);
+          }
         }
-        if (i + 1 < FI) ra = rd(la, xa, i + 1);
-        __builtin_amdgcn_sched_barrier(0);
+        fence();
+      }
+      da[(i + 1) & 1][3] = widen1(ra[0], 3);
+      if constexpr (kHead) {
 #pragma unroll
-        for (int j = 0; j < FJ; ++j) {
-          const int g = i * FJ + j;
-          v16f tt = v16f{};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) tt = __builtin_amdgcn_mfma_f32_32x32x16_f16(db[j][e], da[e], tt, 0, 0, 0);
-          tm[g & 1] = tt;
-          issue(g, G);
-          __builtin_amdgcn_sched_barrier(0);
-          if (g > 0) add((g - 1) / FJ, (g - 1) % FJ, tm[(g - 1) & 1]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int j = 0; j < FJ; ++j) db[j][3] = widen1(rb[j], 3);
       }
     }
-    add(FI - 1, FJ - 1, tm[(G - 1) & 1]);
   };
+  // Keeps the sums ahead of what follows: the compiler would otherwise sink
+  // them past the branches there and hold a temporary for every fragment.
+  auto pin = [&]() {
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+      for (int j = 0; j < FJ; ++j) asm volatile("" : "+v"(acc[i][j]));
+  };
+  auto body = [&](auto self, auto ic) -> void {
+    constexpr int i = decltype(ic)::value;
+    if constexpr (i < FI - 1) {
+      row(ic);
+      self(self, std::integral_constant<int, i + 1>());
+    }
+  };
+  static_assert(FI >= 2 && FI % 2 == 0 && FJ == 4, "A's two fragment buffers alternate across steps");
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) acc[i][j] = v16f{};
+      for (int j = 0; j < FJ; ++j) acc[i][j] = v4f{};
   };
 
-  int round = 0, k = 0;
-  Tile t = make_tile<C>(p, table, ord, tile_at(0));
+  int round = 0;
+  bool have = false;            // the current step's first fragments are in registers
+  Tile t = tile_of(0);
   clear();
   for (;;) {
+    const int nk = t.nk > 0 ? t.nk : 1;
     // A wave whose rows all lie past the tile's last one only loads its share.
     const bool active = t.row0 + wm * C::WTM < t.row_end;
-    issue_scales();
+    auto next = [&](int k) {     // ends step k: the next step's loads have landed
+      advance();
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage has been read
+      land();
+      stage = stage + 1 == ST ? 0 : stage + 1;
+      if (k + 1 == nk || (C::GROUPED && (k & 3) == 3)) group ^= 1;
+    };
     if (active) {
-      step(t, k);
-    } else {
+      if (!have) read_first();
+      flast = 0.0f;
 #pragma unroll
-      for (int s = 0; s < G; ++s) issue(s, G);
+      for (int j = 0; j < FJ; ++j) tm[D - 1][j] = v4f{};
+      for (int k = 0; k < nk; ++k) {
+        issue_scales();
+        read_f(t, k);
+        body(body, std::integral_constant<int, 0>());
+        pin();
+        next(k);
+        row(std::integral_constant<int, FI - 1>());
+        pin();
+        flast = f[FI - 1];
+      }
+      if constexpr (C::FAST) {
+        add(FI - 1, FJ - 2, flast);
+        add(FI - 1, FJ - 1, flast);
+      } else {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) add(FI - 1, j, flast);
+      }
+    } else {
+      for (int k = 0; k < nk; ++k) {
+        issue_scales();
+#pragma unroll
+        for (int s = 0; s < LS; ++s) issue(s, LS);
+        next(k);
+      }
     }
-    advance();
-    land();
-    stage = stage + 1 == ST ? 0 : stage + 1;
-    ++k;
-    if (k < t.nk) {
-      if (C::GROUPED && (k & 3) == 0) group ^= 1;
-      continue;
-    }
-    group ^= 1;
-    k = 0;
+    have = active;
 
     // ------------------------------------------------------------ epilogue
-    // lane: row r32 of each fragment; accumulator 4 b + e is column 8 b + 4 h + e
+    // lane: row x16 of each fragment row; a pair of fragments holds columns
+    // 32 jp + 8 q + 0 .. 7
     if (active) {
-    int ln = lane;                       // opaque: nothing below is kept through the K loop
-    asm volatile("" : "+v"(ln));
-    const int h = ln >> 5, r32 = ln & 31;
-    const int64_t orow = (p.form == kGroupK ? (int64_t)t.g * p.rows : 0) + (int64_t)t.slice * p.rows;
+      int ln = lane;                       // opaque: nothing below is kept through the K loop
+      asm volatile("" : "+v"(ln));
+      const int x16 = ln & 15, q = ln >> 4;
+      constexpr int ES = OUT == kOutBf16 || OUT == kOutF16 ? 2 : 4;
+      const int64_t orow = (p.form == kGroupK ? (int64_t)t.g * p.rows : 0) + (int64_t)t.slice * p.rows;
+      int64_t row = t.row0 + wm * C::WTM + x16;
+      const int64_t n = t.n0 + wn * C::WTN + 8 * q;
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + ((orow + row) * p.n + n) * ES;
 #pragma unroll
-    for (int i = 0; i < FI; ++i) {
-      const int64_t row = t.row0 + wm * C::WTM + 32 * i + r32;
-      const bool rin = row < t.row_end;
-      const int64_t o = (orow + row) * p.n;
+      for (int i = 0; i < FI; ++i) {
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) {
-        const int64_t nb = t.n0 + wn * C::WTN + 32 * j;
-        if constexpr (OUT == kOutBf16 || OUT == kOutF16) {
-          // lanes l and l ^ 32 trade quads, so that each holds 8 columns of two of the four octets
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t e0 = pack_half2<OUT == kOutF16>(acc[i][j][8 * q], acc[i][j][8 * q + 1]);
-            uint32_t e1 = pack_half2<OUT == kOutF16>(acc[i][j][8 * q + 2], acc[i][j][8 * q + 3]);
-            uint32_t o0 = pack_half2<OUT == kOutF16>(acc[i][j][8 * q + 4], acc[i][j][8 * q + 5]);
-            uint32_t o1 = pack_half2<OUT == kOutF16>(acc[i][j][8 * q + 6], acc[i][j][8 * q + 7]);
-            auto s0_ = __builtin_amdgcn_permlane32_swap(e0, o0, false, false);
-            auto s1_ = __builtin_amdgcn_permlane32_swap(e1, o1, false, false);
-            const int64_t n = nb + 16 * q + 8 * h;
-            if (rin && n < p.n)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o + n) =
-                  make_uint4(s0_[0], s1_[0], s0_[1], s1_[1]);
-          }
-        } else {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int64_t n = nb + 8 * b + 4 * h;
-            v4f v{acc[i][j][4 * b], acc[i][j][4 * b + 1], acc[i][j][4 * b + 2], acc[i][j][4 * b + 3]};
-            if (rin && n < p.n) {
-              v4f* d = reinterpret_cast<v4f*>(static_cast<float*>(p.out) + o + n);
-              if constexpr (OUT == kOutF32Add) v = *d + v;
-              *d = v;
+        for (int jp = 0; jp < FJ / 2; ++jp) {
+          if (row < t.row_end && n + 32 * jp < p.n) {
+            const v4f lo4 = acc[i][2 * jp], hi4 = acc[i][2 * jp + 1];
+            if constexpr (ES == 2) {
+              constexpr bool F16 = OUT == kOutF16;
+              reinterpret_cast<uint4*>(dst)[4 * jp] =
+                  make_uint4(pack_half2<F16>(lo4[0], lo4[1]), pack_half2<F16>(lo4[2], lo4[3]),
+                             pack_half2<F16>(hi4[0], hi4[1]), pack_half2<F16>(hi4[2], hi4[3]));
+            } else {
+              v4f* d = reinterpret_cast<v4f*>(dst) + 8 * jp;
+              if constexpr (OUT == kOutF32Add) {
+                const v4f a0 = d[0], a1 = d[1];
+                d[0] = a0 + lo4;
+                d[1] = a1 + hi4;
+              } else {
+                d[0] = lo4;
+                d[1] = hi4;
+              }
             }
           }
         }
+        row += 16;
+        dst += 16 * p.n * ES;
+        fence();
       }
     }
-    }
+    if (tile_at(++round) >= last) break;
+    plan(round + ST - 1);
+    t = tile_of(round);
     clear();
-    const int id = tile_at(++round);
-    if (id >= last) break;
-    t = make_tile<C>(p, table, ord, id);
   }
   wait_vm<0>();       // no load may land in LDS after the workgroup has ended
 }
