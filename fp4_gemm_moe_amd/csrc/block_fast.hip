@@ -9,6 +9,7 @@ hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const Device
   using namespace blk;
   switch (tile) {
     case kTile256x256: return launch_out<Cfg<256, 256, 2, 4, 2, true>, kOutBf16, kOutF32>(s, p, dev, nt);
+    case kTile128x256: return launch_out<Cfg<128, 256, 2, 4, 3, true>, kOutBf16, kOutF32>(s, p, dev, nt);
     case kTile128x128: return launch_out<Cfg<128, 128, 2, 2, 4, true>, kOutBf16, kOutF32>(s, p, dev, nt);
     default: return launch_out<Cfg<64, 128, 2, 2, 5, true>, kOutBf16, kOutF32>(s, p, dev, nt);
   }

@@ -8,6 +8,8 @@
 // step from zero, and the vector unit adds that sum times sa sb to the FP32
 // accumulator.  The scales are per row of a and per 128 columns, so a lane's
 // factor is one product for all accumulators of its row.
+#include <algorithm>
+
 #include "block_launch.hpp"
 #include "hq.h"
 
@@ -15,187 +17,253 @@ namespace hq {
 namespace {
 
 // ------------------------------------------------------------------ direct
-// A workgroup of W waves takes 16 MF rows x 16 NF columns; its waves take the
-// K blocks in turn, each lane loading its operands from global memory, and
-// their sums meet in LDS.
-template <int MF, int NF, int W>
+// Few rows: the weights are read once and bound the call.  A workgroup of W
+// waves takes 16 MF rows x 16 columns of one batch item; its waves take runs
+// of U K blocks in turn, each lane loading its operands from global memory
+// (U blocks in flight, the weights with the non-temporal policy), and their
+// sums meet in LDS.
+template <int MF, int NF, int W, int U>
 __global__ __launch_bounds__(W * 64) void block_gemm_direct(BlockGemmArgs p) {
-  __shared__ int ends[kMaxGroups];
-  __shared__ v4f part[W > 1 ? W - 1 : 1][MF * NF][64];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  __shared__ v4f part[W - 1][MF * NF][64];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q = lane >> 4;
-  const int g = blockIdx.y;
-  int64_t row0 = 0, row_end = p.rows;
-  int kb0 = 0, kb1 = p.nkb;
-  if (p.form == kContiguous || p.form == kGroupK) {
-    load_clamped_ends<W * 64>(ends, p.group_end, p.groups, p.form == kContiguous ? p.rows : p.k);
-    const int lo = g > 0 ? ends[g - 1] : 0, hi = ends[g];
-    if (p.form == kContiguous) {
-      row0 = lo;
-      row_end = hi;
-    } else {
-      kb0 = lo / 128;
-      kb1 = hi / 128;
-    }
-  } else {
-    row0 = g * p.slot_rows;
-    int64_t c = p.slot_rows;
-    if (p.form == kMasked) {
-      c = p.counts[g];
-      c = c < 0 ? 0 : (c > p.slot_rows ? p.slot_rows : c);
-    }
-    row_end = row0 + c;
-  }
+  const int64_t g = blockIdx.y, row0 = g * p.slot_rows, row_end = row0 + p.slot_rows;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * NF;
-  const bool own_b = p.form != kGroupK;
-  const uint8_t* b = p.b + (own_b ? (int64_t)g * p.n * p.k : 0);
-  const float* sb = p.sb + (own_b ? (int64_t)g * p.nnb * p.nkb : 0) + (n0 / 128) * p.nkb;
+  const float* sb = p.sb + (g * p.nnb + n0 / 128) * p.nkb;
   const uint8_t* bp[NF];
 #pragma unroll
   for (int j = 0; j < NF; ++j) {
-    const int64_t n = n0 + 16 * j + r16;
-    bp[j] = b + (n < p.n ? n : p.n - 1) * p.k;
+    const int64_t nb = n0 + 16 * j + r16;
+    bp[j] = p.b + (g * p.n + (nb < p.n ? nb : p.n - 1)) * p.k + 16 * q;
   }
-  for (int64_t m0 = row0 + (int64_t)blockIdx.z * 16 * MF; m0 < row_end; m0 += (int64_t)gridDim.z * 16 * MF) {
-    const uint8_t* ap[MF];
-    const float* sap[MF];
+  const uint8_t* ap[MF];
+  const float* sap[MF];
+  v4f acc[MF][NF];
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      const int64_t r = m0 + 16 * i + r16;
-      ap[i] = p.a + (r < row_end ? r : row_end - 1) * p.k;
-      sap[i] = p.sa + (r < row_end ? r : row_end - 1) * p.nkb;
-    }
-    v4f acc[MF][NF];
+  for (int i = 0; i < MF; ++i) {
+    const int64_t r = row0 + 16 * i + r16, rr = r < row_end ? r : row_end - 1;
+    ap[i] = p.a + rr * p.k + 16 * q;
+    sap[i] = p.sa + rr * p.nkb;
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
+    for (int j = 0; j < NF; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+  }
+  const int k16 = (int)p.k - 16 * q;           // codes of a row from the lane's first one on
+  for (int kb = w * U; kb < p.nkb; kb += W * U) {
+    v8i bf[NF][U], af[MF][U];
+    float sv[U], sav[MF][U];
 #pragma unroll
-      for (int j = 0; j < NF; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    for (int kb = kb0 + w; kb < kb1; kb += W) {
-      const int64_t k0 = (int64_t)kb * 128 + 16 * q;
-      const bool in0 = k0 < p.k, in1 = k0 + 64 < p.k;
-      v8i bf[NF];
+    for (int u = 0; u < U; ++u) {
+      const int k0 = (kb + u) * 128;
 #pragma unroll
-      for (int j = 0; j < NF; ++j) bf[j] = load_pair(bp[j] + k0, in0, in1);
-      const float sbv = sb[kb];
+      for (int j = 0; j < NF; ++j) bf[j][u] = load_pair<false>(bp[j] + k0, k0 < k16, k0 + 64 < k16);
+      sv[u] = kb + u < p.nkb ? sb[kb + u] : 0.0f;
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        const v8i af = load_pair(ap[i] + k0, in0, in1);
-        const float f = sap[i][kb] * sbv;
+        af[i][u] = load_pair<false>(ap[i] + k0, k0 < k16, k0 + 64 < k16);
+        sav[i][u] = kb + u < p.nkb ? sap[i][kb + u] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        const float f = sav[i][u] * sv[u];
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          const v4f t = dot16(bf[j], af);
+          const v4f t = dot16(bf[j][u], af[i][u]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t[e], f, acc[i][j][e]);
         }
       }
-    }
-    if (W > 1) {
-      __syncthreads();
-      if (w > 0)
+  }
+  if (w > 0) {
 #pragma unroll
-        for (int i = 0; i < MF; ++i)
+    for (int i = 0; i < MF * NF; ++i) part[w - 1][i][lane] = acc[i / NF][i % NF];
+  }
+  __syncthreads();
+  if (w == 0) {
 #pragma unroll
-          for (int j = 0; j < NF; ++j) part[w - 1][i * NF + j][lane] = acc[i][j];
-      __syncthreads();
-    }
-    if (w == 0) {
+    for (int i = 0; i < MF * NF; ++i) {
+      v4f v = acc[i / NF][i % NF];
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-          v4f v = acc[i][j];
-          for (int o = 0; o < W - 1; ++o) v += part[o][i * NF + j][lane];
-          const int64_t r = m0 + 16 * i + r16, n = n0 + 16 * j + 4 * q;
-          if (r < row_end && n < p.n)
-            store4(p.out, p.out_kind, ((p.form == kGroupK ? (int64_t)g * p.rows : 0) + r) * p.n + n, v);
-        }
+      for (int o = 0; o < W - 1; ++o) v += part[o][i][lane];
+      const int64_t r = row0 + 16 * (i / NF) + r16, n = n0 + 16 * (i % NF) + 4 * q;
+      if (r < row_end && n < p.n) store4(p.out, p.out_kind, r * p.n + n, v);
     }
   }
 }
 
 // ------------------------------------------------------------------ K split
-// out = the slices' FP32 partial sums, added in slice order.
+// out = the slices' FP32 partial sums [slices, rows, n], added in slice order.
 constexpr int kReduceThreads = 256;
 __global__ __launch_bounds__(kReduceThreads) void block_reduce(const float* __restrict__ partial, int slices,
-                                                               int64_t quads, void* out, int32_t kind) {
-  const int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x;
+                                                               int64_t rows, uint32_t nq, int64_t ldo, void* out,
+                                                               int32_t kind) {
+  const int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x, quads = rows * nq;
   if (i >= quads) return;
   const v4f* src = reinterpret_cast<const v4f*>(partial) + i;
   v4f v = src[0];
   for (int s = 1; s < slices; ++s) v += src[s * quads];
-  store4(out, kind, 4 * i, v);
+  const int64_t row = i / nq;
+  store4(out, kind, row * ldo + 4 * (i - row * nq), v);
 }
 
+// ------------------------------------------------------------------ plan
+// BF16 results of four K blocks or more take the FP8 matrix instructions: their
+// sums are off by 1.5e-5 of the norm at K = 128 and less with every further
+// block, a hundredth of the BF16 rounding at four.  Shorter sums, and FP16 and
+// FP32 results, go through FP16 operands with full FP32 sums.
 bool fast_path(const BlockGemmArgs& p) { return p.out_kind == kOutBf16 && p.nkb >= 4; }
 
+// A tile shape and what one of its steps takes on a full chip (microseconds,
+// measured at 2048 and 4096 x 17408 x 5120).
+struct Shape {
+  int tile, bm, bn;
+  double us;
+};
+constexpr Shape kFast[] = {{kTile256x256, 256, 256, 2.13}, {kTile128x256, 128, 256, 1.30},
+                           {kTile128x128, 128, 128, 0.80}, {kTile64x128, 64, 128, 0.65}};
+constexpr Shape kExact[] = {{kTile256x128, 256, 128, 2.60}, {kTile128x128, 128, 128, 1.40}, {kTile64x128, 64, 128, 0.90}};
+
+constexpr double kBytesPerUs = 5.0e6;      // HBM, of the partial sums and of weights that are read once
+constexpr double kLaunchUs = 3.0;          // a further launch on the stream
+
+// How a launch over n columns is tiled, and its estimated time.
 struct Plan {
-  bool direct;
-  int tile;
-  int slices;
-  uint64_t bytes;      // workspace of the split
+  int tile = kTile256x256;
+  int slices = 1;
+  double us = 1e30;
+  uint64_t bytes(int64_t rows, int64_t n) const { return slices > 1 ? (uint64_t)slices * rows * n * 4 : 0; }
 };
 
-Plan plan_gemm(const BlockGemmArgs& p, const DeviceInfo& dev) {
-  Plan pl{false, kTile256x256, 1, 0};
-  const bool fast = fast_path(p);
-  const int64_t per = p.form == kContiguous ? (p.rows + p.groups - 1) / p.groups
-                                            : (p.form == kGroupK ? p.rows : p.slot_rows);
-  if (p.form == kUniform && p.slot_rows <= 16) {
-    pl.direct = true;
-    return pl;
-  }
-  int bm = 256, bn = 256;
-  if (per <= 64 || p.nkb < 4) {        // the larger tiles fetch four K blocks' scales at a time
-    pl.tile = kTile64x128;
-    bm = 64, bn = 128;
-  } else if (fast && per <= 128) {
-    pl.tile = kTile128x128;
-    bm = 128, bn = 128;
-  } else if (!fast) {
-    pl.tile = kTile256x128;
-    bn = 128;
-  }
-  if (p.form == kUniform) {
-    const int64_t tiles = (p.slot_rows + bm - 1) / bm * p.groups * ((p.n + bn - 1) / bn);
-    int64_t s = dev.num_cus / tiles;
-    if (s > p.nkb / 4) s = p.nkb / 4;
-    const int64_t most = (int64_t)(HQ_BLOCK_WORKSPACE_BYTES / 4) / (p.rows * p.n);
-    if (s > most) s = most;
-    if (s > 1) {
-      pl.slices = (int)s;
-      pl.bytes = (uint64_t)s * p.rows * p.n * 4;
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Uniform rows: the shape and K split with the least estimated time, rounds of
+// the chip x steps x step time, plus what writing, reading and adding up the
+// partial sums takes.  A step whose weights no other m-tile shares takes at
+// least their time from memory.
+Plan plan_uniform(const BlockGemmArgs& p, int64_t n, const DeviceInfo& dev, bool fast, uint64_t ws) {
+  Plan best;
+  const int64_t cus = dev.num_cus;
+  auto consider = [&](const Shape& sh) {
+    if (sh.tile != kTile64x128 && p.nkb < 4) return;      // they fetch four K blocks' scales at a time
+    const int64_t mt = up(p.slot_rows, sh.bm), tiles = mt * p.groups * up(n, sh.bn);
+    for (int s = 1; s <= 16 && (s == 1 || s * 4 <= p.nkb); ++s) {
+      Plan c;
+      c.tile = sh.tile;
+      c.slices = s;
+      if (c.bytes(p.rows, n) > ws) break;
+      const double stream = mt == 1 ? sh.bn * 128.0 * std::min(tiles * s, cus) / kBytesPerUs : 0.0;
+      c.us = up(up(tiles * s, 8), cus / 8) * up(p.nkb, s) * std::max(sh.us, stream);
+      if (s > 1) c.us += kLaunchUs + 2.0 * c.bytes(p.rows, n) / kBytesPerUs;
+      if (c.us < best.us) best = c;
     }
-  }
+  };
+  if (fast) for (const Shape& sh : kFast) consider(sh);
+  else for (const Shape& sh : kExact) consider(sh);
+  return best;
+}
+
+// One launch over all columns, or two: whole rounds of 256 x 256 tiles over
+// the first `head` columns, then the rest in smaller tiles or K slices, where
+// that is done sooner than a partly filled last round.
+struct Plans {
+  Plan all, rest;
+  int64_t head = 0;      // 0: one launch
+  uint64_t bytes(const BlockGemmArgs& p) const { return head > 0 ? rest.bytes(p.rows, p.n - head) : all.bytes(p.rows, p.n); }
+};
+
+Plans plan_all(const BlockGemmArgs& p, const DeviceInfo& dev, bool fast, uint64_t ws) {
+  Plans pl;
+  pl.all = plan_uniform(p, p.n, dev, fast, ws);
+  if (!fast || p.groups != 1 || pl.all.tile != kTile256x256 || pl.all.slices != 1) return pl;
+  const int64_t mt = up(p.slot_rows, 256), nt = up(p.n, 256), cus = dev.num_cus;
+  const int64_t rounds = mt * nt / cus, head = rounds * cus / mt;
+  if (rounds < 1 || head < 1 || head >= nt) return pl;
+  pl.rest = plan_uniform(p, p.n - head * 256, dev, fast, ws);
+  const double us = up(up(mt * head, 8), cus / 8) * p.nkb * kFast[0].us + kLaunchUs + pl.rest.us;
+  if (us < 0.97 * pl.all.us) pl.head = head * 256;
   return pl;
+}
+
+// Grouped forms, by the rows a group has (on average where only the device
+// knows them): few rows leave the weights' stream to bound the call, which the
+// deeper stages of the smaller tiles serve better; many share each weight tile.
+int plan_grouped(const BlockGemmArgs& p, bool fast) {
+  const int64_t per = p.form == kContiguous ? up(p.rows, p.groups) : (p.form == kGroupK ? p.rows : p.slot_rows);
+  if (p.nkb < 4 || per <= 32) return kTile64x128;
+  if (!fast) return per <= 128 ? kTile128x128 : kTile256x128;
+  const int64_t limit = p.form == kContiguous ? 1024 : 128;
+  return per <= limit ? kTile128x256 : kTile256x256;
+}
+
+bool direct_path(const BlockGemmArgs& p) { return p.form == kUniform && p.slot_rows <= 16; }
+
+hipError_t launch_tiled(hipStream_t s, BlockGemmArgs p, const DeviceInfo& dev, bool fast, const Plan& pl, void* ws) {
+  const BlockGemmArgs whole = p;
+  if (pl.slices > 1) {
+    p.slices = pl.slices;
+    p.out = ws;
+    p.out_kind = kOutF32;
+    p.ldo = p.n;
+  }
+  // weights that one m-tile reads once, by all compute units at once
+  const bool nt = p.form == kMasked && p.slot_rows <= 256;
+  const hipError_t e = fast ? launch_block_fast(s, p, dev, pl.tile, nt) : launch_block_exact(s, p, dev, pl.tile, nt);
+  if (e != hipSuccess || pl.slices == 1) return e;
+  const int64_t quads = p.rows * p.n / 4;
+  hipLaunchKernelGGL(block_reduce, dim3((unsigned)up(quads, kReduceThreads)), dim3(kReduceThreads), 0, s,
+                     static_cast<const float*>(ws), pl.slices, p.rows, (uint32_t)(p.n / 4), whole.ldo, whole.out,
+                     whole.out_kind);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-uint64_t block_gemm_workspace_bytes(const BlockGemmArgs& p, const DeviceInfo& dev) { return plan_gemm(p, dev).bytes; }
+uint64_t block_gemm_workspace_bytes(const BlockGemmArgs& p, const DeviceInfo& dev) {
+  return direct_path(p) ? 0 : plan_all(p, dev, fast_path(p), HQ_BLOCK_WORKSPACE_BYTES).bytes(p);
+}
 
 hipError_t launch_block_gemm(hipStream_t s, const BlockGemmArgs& args, const DeviceInfo& dev, void* workspace,
                              uint64_t workspace_bytes) {
-  const Plan pl = plan_gemm(args, dev);
   BlockGemmArgs p = args;
-  if (pl.direct) {
-    constexpr int MF = 1, NF = 1, W = 8;
-    const dim3 grid((unsigned)((p.n + 16 * NF - 1) / (16 * NF)), (unsigned)p.groups, 1);
-    hipLaunchKernelGGL((block_gemm_direct<MF, NF, W>), grid, dim3(W * 64), 0, s, p);
+  p.ldo = p.n;
+  if (direct_path(p)) {
+    // 16-column workgroups, or 32-column ones where they are many: those read
+    // A half as often (from 6 rows on: 16x17408x5120 30.3 -> 26.4 us, 1 row
+    // 17.6 -> 19.3 us), and where 16 columns would make between one and two
+    // workgroups per compute unit they share the work evenly
+    // (1x5120x17408 22.9 -> 21.0 us, 16 rows 40.4 -> 30.5 us)
+    const int64_t narrow = up(p.n, 16) * p.groups;
+    if (narrow > dev.num_cus && (narrow < 2 * dev.num_cus || p.slot_rows >= 6))
+      hipLaunchKernelGGL((block_gemm_direct<1, 2, 8, 2>), dim3((unsigned)up(p.n, 32), (unsigned)p.groups), dim3(512), 0,
+                         s, p);
+    else
+      hipLaunchKernelGGL((block_gemm_direct<1, 1, 16, 2>), dim3((unsigned)up(p.n, 16), (unsigned)p.groups), dim3(1024), 0,
+                         s, p);
     return hipGetLastError();
   }
-  const bool nt = p.form == kMasked && p.slot_rows <= 256;
-  const bool split = pl.slices > 1 && workspace_bytes >= pl.bytes;
-  if (split) {
-    p.slices = pl.slices;
-    p.out = workspace;
-    p.out_kind = kOutF32;
+  const bool fast = fast_path(p);
+  if (p.form != kUniform) {
+    Plan pl;
+    pl.tile = plan_grouped(p, fast);
+    return launch_tiled(s, p, dev, fast, pl, nullptr);
   }
-  hipError_t e = fast_path(args) ? launch_block_fast(s, p, dev, pl.tile, nt) : launch_block_exact(s, p, dev, pl.tile, nt);
-  if (e != hipSuccess || !split) return e;
-  const int64_t quads = p.rows * p.n / 4;
-  hipLaunchKernelGGL(block_reduce, dim3((unsigned)((quads + kReduceThreads - 1) / kReduceThreads)), dim3(kReduceThreads),
-                     0, s, static_cast<const float*>(workspace), pl.slices, quads, args.out, args.out_kind);
-  return hipGetLastError();
+  // the plan that HQ_BLOCK_WORKSPACE_BYTES would allow if the workspace holds
+  // it, else the best one without a split
+  Plans pl = plan_all(p, dev, fast, HQ_BLOCK_WORKSPACE_BYTES);
+  if (pl.bytes(p) > (workspace != nullptr ? workspace_bytes : 0)) pl = plan_all(p, dev, fast, 0);
+  if (pl.head == 0) return launch_tiled(s, p, dev, fast, pl.all, workspace);
+  const int64_t head = pl.head;
+  BlockGemmArgs first = p, rest = p;
+  first.n = head;
+  const hipError_t e = launch_tiled(s, first, dev, fast, pl.all, nullptr);
+  if (e != hipSuccess) return e;
+  rest.n = p.n - head;
+  rest.b += head * p.k;
+  rest.sb += head / 128 * p.nkb;
+  rest.out = static_cast<uint8_t*>(p.out) + head * (p.out_kind == kOutF32 || p.out_kind == kOutF32Add ? 4 : 2);
+  return launch_tiled(s, rest, dev, fast, pl.rest, workspace);
 }
 
 }  // namespace hq

@@ -34,12 +34,14 @@ __device__ __forceinline__ v4f dot16(v8i w, v8i x) {
   return acc;
 }
 
-// The 16 bytes at p and the 16 at p + 64; zeros where the flag is off.
+// The 16 bytes at p and the 16 at p + 64; zeros where the flag is off.  NT:
+// with the non-temporal policy.
+template <bool NT>
 __device__ __forceinline__ v8i load_pair(const uint8_t* p, bool in0, bool in1) {
-  uint4 u = make_uint4(0, 0, 0, 0), v = u;
-  if (in0) u = *reinterpret_cast<const uint4*>(p);
-  if (in1) v = *reinterpret_cast<const uint4*>(p + 64);
-  return v8i{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+  v4i u = {0, 0, 0, 0}, v = u;
+  if (in0) u = NT ? __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p)) : *reinterpret_cast<const v4i*>(p);
+  if (in1) v = NT ? __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p + 64)) : *reinterpret_cast<const v4i*>(p + 64);
+  return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // Four consecutive results at element `at` of the output.

@@ -27,6 +27,7 @@ struct BlockGemmArgs {
   int64_t rows;              // rows of a (all groups)
   int64_t slot_rows;         // kUniform, kMasked: rows of a group
   int64_t n, k;
+  int64_t ldo;               // elements from row to row of out
   int32_t nkb, nnb;          // ceil(k / 128), ceil(n / 128)
   int32_t groups;
   int32_t form;

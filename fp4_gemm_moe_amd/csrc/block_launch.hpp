@@ -9,7 +9,7 @@
 namespace hq {
 
 // Tile shapes of the tiled kernel (rows x columns).
-enum BlockTile : int { kTile256x256, kTile256x128, kTile128x128, kTile64x128 };
+enum BlockTile : int { kTile256x256, kTile256x128, kTile128x256, kTile128x128, kTile64x128 };
 
 hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, bool nt);
 hipError_t launch_block_exact(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, bool nt);

@@ -639,7 +639,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
       const int64_t orow = (p.form == kGroupK ? (int64_t)t.g * p.rows : 0) + (int64_t)t.slice * p.rows;
       int64_t row = t.row0 + wm * C::WTM + x16;
       const int64_t n = t.n0 + wn * C::WTN + 8 * q;
-      uint8_t* dst = static_cast<uint8_t*>(p.out) + ((orow + row) * p.n + n) * ES;
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + ((orow + row) * p.ldo + n) * ES;
 #pragma unroll
       for (int i = 0; i < FI; ++i) {
 #pragma unroll
@@ -665,7 +665,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
           }
         }
         row += 16;
-        dst += 16 * p.n * ES;
+        dst += 16 * p.ldo * ES;
         fence();
       }
     }
