@@ -15,23 +15,27 @@ namespace hq {
 namespace {
 
 // ------------------------------------------------------------------ sort
-// A stable counting sort.  A workgroup takes a run of `chunk` consecutive
-// pairs, each of its 16 waves a sixteenth of the run.  A wave counts its
-// pairs per expert in LDS, the counts become each wave's first row per
-// expert, and the wave walks its pairs again in order, 64 at a time: a lane's
-// row is the wave's next row of its expert plus the number of lower lanes
-// with the same expert (a mask built from one ballot per id bit).
+// A stable counting sort.  A workgroup takes a run of consecutive pairs, each
+// of its waves an equal part of the run, 64 pairs a step.  A wave counts its
+// pairs per expert in LDS, the counts become each wave's first row per expert,
+// and the wave walks its pairs again in order: a lane's row is the wave's next
+// row of its expert plus the number of lower lanes with the same expert (a
+// mask built from one ballot per id bit).  A wave holds its first kHeld steps'
+// ids in registers between the two walks.
 // With more than one workgroup a first launch leaves every workgroup's counts
 // in the workspace, and each workgroup of the second adds up what lies ahead
-// of it.  The work is a few bytes a pair: launches and latency bound it.
+// of it.  The work is a few bytes a pair: launches and latency bound it, so a
+// run is as short as the workgroups can cover (one step a wave up to 1024
+// pairs: 512 pairs of 64 experts 13.6 us with runs of four steps, see below).
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int64_t kSortChunk = 4096;       // pairs of a workgroup, at least
+constexpr int kHeld = 4;
 constexpr int kSortMaxBlocks = 256;
 
+// Pairs of a workgroup's run: up to 4096 in one workgroup, else at least 2048.
 int64_t sort_chunk(int64_t pairs) {
-  int64_t c = (pairs + kSortMaxBlocks - 1) / kSortMaxBlocks;
-  c = c < kSortChunk ? kSortChunk : c;
-  return (c + kSortThreads - 1) / kSortThreads * kSortThreads;
+  if (pairs <= kSortThreads * kHeld) return pairs > 0 ? (pairs + kSortThreads - 1) / kSortThreads * kSortThreads : kSortThreads;
+  const int64_t c = (pairs + kSortMaxBlocks - 1) / kSortMaxBlocks, least = 2 * kSortThreads;
+  return ((c < least ? least : c) + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
 __device__ __forceinline__ int pair_expert(const int64_t* ids, int64_t i, int64_t end, int E) {
@@ -54,8 +58,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_count(const int64_t* __rest
   for (int e = threadIdx.x; e < E; e += kSortThreads) ws[(int64_t)blockIdx.x * E + e] = cnt[e];
 }
 
-// Dynamic LDS: wave counts [16][E], then per expert its total (then its
-// inclusive end), its first row and the rows ahead of this workgroup.
+// Dynamic LDS: wave counts [16][E], then per expert its total, its inclusive
+// padded end and the rows ahead of this workgroup.
 __global__ __launch_bounds__(kSortThreads) void sort_place(const int64_t* __restrict__ ids, int64_t pairs, int E,
                                                            int align, int64_t chunk, int64_t max_rows,
                                                            const int32_t* __restrict__ ws,
@@ -66,55 +70,59 @@ __global__ __launch_bounds__(kSortThreads) void sort_place(const int64_t* __rest
   extern __shared__ int32_t sh[];
   int32_t* wc = sh;                         // [16][E]
   int32_t* total = sh + kSortWaves * E;     // [E]
-  int32_t* end = total + E;                 // [E] inclusive padded ends
+  int32_t* end = total + E;                 // [E]
   int32_t* ahead = end + E;                 // [E]
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int nb = gridDim.x;
-  for (int e = tid; e < (kSortWaves + 3) * E; e += kSortThreads) sh[e] = 0;
-  __syncthreads();
   const int64_t b0 = blockIdx.x * chunk, b1 = b0 + chunk < pairs ? b0 + chunk : pairs;
   const int64_t per = chunk / kSortWaves;
   const int64_t w0 = b0 + w * per, w1 = w0 + per < b1 ? w0 + per : b1;
-  for (int64_t i = w0 + lane; i < w1; i += 64) {
+  int held[kHeld];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) held[h] = h * 64 < per ? pair_expert(ids, w0 + h * 64 + lane, w1, E) : -1;
+  // where the counts of earlier workgroups come from: threads in parts of at
+  // least E, part p adds up workgroups p, p + parts, ..
+  int wide = 64;
+  while (wide < E) wide <<= 1;
+  int all = 0, pre = 0;
+  const int parts = kSortThreads / wide, pe = tid & (wide - 1);
+  if (nb > 1 && pe < E)
+    for (int b = tid / wide; b < nb; b += parts) {
+      const int v = ws[(int64_t)b * E + pe];
+      all += v;
+      pre += b < (int)blockIdx.x ? v : 0;
+    }
+  for (int e = tid; e < (kSortWaves + 3) * E; e += kSortThreads) sh[e] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (held[h] >= 0) atomicAdd(wc + w * E + held[h], 1);
+  for (int64_t i = w0 + kHeld * 64 + lane; i < w1; i += 64) {
     const int e = pair_expert(ids, i, w1, E);
     if (e >= 0) atomicAdd(wc + w * E + e, 1);
   }
-  if (nb > 1) {
-    // threads in parts of at least E: part p adds up workgroups p, p + parts, ..
-    int wide = 64;
-    while (wide < E) wide <<= 1;
-    const int parts = kSortThreads / wide, e = tid & (wide - 1);
-    if (e < E) {
-      int all = 0, pre = 0;
-      for (int b = tid / wide; b < nb; b += parts) {
-        const int v = ws[(int64_t)b * E + e];
-        all += v;
-        pre += b < (int)blockIdx.x ? v : 0;
-      }
-      atomicAdd(total + e, all);
-      atomicAdd(ahead + e, pre);
-    }
+  if (nb > 1 && pe < E) {
+    atomicAdd(total + pe, all);
+    atomicAdd(ahead + pe, pre);
   }
   __syncthreads();
-  if (nb == 1) {
-    for (int e = tid; e < E; e += kSortThreads) {
-      int s = 0;
-      for (int v = 0; v < kSortWaves; ++v) s += wc[v * E + e];
-      total[e] = s;
+  // per expert: the waves' counts become counts before each wave
+  for (int e = tid; e < E; e += kSortThreads) {
+    int c[kSortWaves], s = 0;
+#pragma unroll
+    for (int v = 0; v < kSortWaves; ++v) c[v] = wc[v * E + e];
+#pragma unroll
+    for (int v = 0; v < kSortWaves; ++v) {
+      wc[v * E + e] = s;
+      s += c[v];
     }
-    __syncthreads();
+    if (nb == 1) total[e] = s;
+    end[e] = (total[e] + align - 1) / align * align;
   }
-  for (int e = tid; e < E; e += kSortThreads) end[e] = (total[e] + align - 1) / align * align;
   __syncthreads();
   const int last = block_scan_1024<kSortThreads>(end, E, OpAdd(), 0);
   for (int e = tid; e < E; e += kSortThreads) {
-    const int start = e > 0 ? end[e - 1] : 0;
-    int next = start + ahead[e];
-    for (int v = 0; v < kSortWaves; ++v) {          // a wave's count -> its next row
-      const int c = wc[v * E + e];
-      wc[v * E + e] = next;
-      next += c;
-    }
+    ahead[e] += e > 0 ? end[e - 1] : 0;             // the workgroup's first row of the expert
     if (blockIdx.x == 0) {
       group_end[e] = end[e];
       counts[e] = total[e];
@@ -124,9 +132,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place(const int64_t* __rest
   int bits = 1;
   while ((1 << bits) < E) ++bits;
   int32_t* mine = wc + w * E;
-  for (int64_t i0 = w0; i0 < w1; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const int e = pair_expert(ids, i, w1, E);
+  auto place = [&](int64_t i, int e) {
     uint64_t same = __ballot(e >= 0);
     for (int b = 0; b < bits; ++b) {
       const uint64_t m = __ballot((e >> b) & 1);
@@ -134,19 +140,24 @@ __global__ __launch_bounds__(kSortThreads) void sort_place(const int64_t* __rest
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
     int row = -1;
-    if (e >= 0) row = mine[e] + rank;
+    if (e >= 0) row = ahead[e] + mine[e] + rank;
     __builtin_amdgcn_wave_barrier();
-    if (e >= 0 && rank == 0) mine[e] = row + __popcll(same);
+    if (e >= 0 && rank == 0) mine[e] += __popcll(same);
     __builtin_amdgcn_wave_barrier();
     if (i < w1) {
       row_map[i] = row;
       if (row >= 0 && row < max_rows) row_pair[row] = (int32_t)i;
     }
-  }
-  // rows that no pair takes: each group's padding, and what follows the last end
-  for (int g = blockIdx.x; g < E; g += nb) {
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (w0 + h * 64 < w1) place(w0 + h * 64 + lane, held[h]);
+  for (int64_t i0 = w0 + kHeld * 64; i0 < w1; i0 += 64) place(i0 + lane, pair_expert(ids, i0 + lane, w1, E));
+  // rows that no pair takes: each group's padding, a wave a group, and what
+  // follows the last end
+  for (int g = blockIdx.x * kSortWaves + w; g < E; g += nb * kSortWaves) {
     const int start = (g > 0 ? end[g - 1] : 0) + total[g];
-    for (int64_t r = start + tid; r < end[g] && r < max_rows; r += kSortThreads) row_pair[r] = -1;
+    for (int64_t r = start + lane; r < end[g] && r < max_rows; r += 64) row_pair[r] = -1;
   }
   for (int64_t r = last + (int64_t)blockIdx.x * kSortThreads + tid; r < max_rows; r += (int64_t)nb * kSortThreads)
     row_pair[r] = -1;
