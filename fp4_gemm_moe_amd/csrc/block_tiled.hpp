@@ -41,9 +41,14 @@ __device__ __forceinline__ const T* uniform(const T* p) {
   return reinterpret_cast<const T*>(ufirst64((int64_t)(uintptr_t)p));
 }
 
-// XOR swizzle of the eight 16-byte chunks of a 128-byte LDS row: the 32 rows
-// of a half wave's fragment read fall on all banks evenly.
-__device__ __forceinline__ int swz(int row) { return (row ^ (row >> 3)) & 7; }
+// XOR swizzles of the eight 16-byte chunks of a 128-byte LDS row.  Two rows
+// cover the 64 banks, so the rows of one parity that a 16-lane group of a
+// fragment read touches need different slots: A's fragments are 16 rows in
+// order, B's take rows 8 a + 4 e + b (a, b < 4; below).  With the swizzle that
+// suits 32-row fragments, (row ^ row / 8) % 8, half of the LDS cycles were
+// conflicts.
+__device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swz_b(int row) { return ((row >> 2) & 6) | ((row >> 1) & 1); }
 
 // Raw buffer descriptor over [base, base + bytes).  A tile's operands take
 // less than 2^31 bytes, so an offset with bit 31 set lies outside.
@@ -279,18 +284,19 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
 
   // Load offsets, the same for every tile and step: load i of wave w fills
   // LDS rows (i WAVES + w) 8 .. + 7, lane j the chunk that belongs at slot
-  // j % 8 of row j / 8.  With eight waves the swizzle does not depend on i, so
-  // one offset serves all loads and the descriptor moves by i 64 rows.
-  constexpr bool ONE = C::WAVES % 8 == 0;
-  constexpr int OL = ONE ? 1 : (AL > BL ? AL : BL);
-  uint32_t off[OL], drop = 0;        // drop: loads whose chunk lies past the last, partial K block's end
-  const uint32_t krem = (uint32_t)p.k & 127;
-#pragma unroll
-  for (int i = 0; i < OL; ++i) {
-    const uint32_t row = (i * C::WAVES + w) * 8 + (lane >> 3), c = (lane & 7) ^ swz(row);
-    off[i] = row * (uint32_t)p.k + c * 16;
-    drop |= (krem != 0 && c * 16 >= krem ? 1u : 0u) << i;
+  // j % 8 of row j / 8.  The swizzles do not depend on i (WAVES is a multiple of
+  // 4), so one offset serves all loads of an operand and the descriptor moves.
+  uint32_t offa, offb;               // bit 31 drops a load
+  uint32_t dropa, dropb;             // its value for chunks past the last, partial K block's end
+  {
+    const uint32_t krem = (uint32_t)p.k & 127, row = w * 8 + (lane >> 3);
+    const uint32_t ca = ((lane & 7) ^ swz_a(row)) * 16, cb = ((lane & 7) ^ swz_b(row)) * 16;
+    offa = row * (uint32_t)p.k + ca;
+    offb = row * (uint32_t)p.k + cb;
+    dropa = krem != 0 && ca >= krem ? 0x80000000u : 0u;
+    dropb = krem != 0 && cb >= krem ? 0x80000000u : 0u;
   }
+  static_assert(C::WAVES % 4 == 0, "the swizzles' period");
   const uint32_t hop = (uint32_t)p.k * (C::WAVES * 8);      // bytes from one load's rows to the next one's
   const uint32_t lds0 = ufirst((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)smem);
 
@@ -352,22 +358,21 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     const int kb = lkb0 + lk;
     const uint32_t st = lds0 + (uint32_t)lstep * C::STAGE + (uint32_t)w * 1024;
     const uint32_t ko = (uint32_t)kb * 128;
-    const uint32_t d = kb == p.nkb - 1 ? drop : 0u;
+    const bool tail = kb == p.nkb - 1;
+    const uint32_t va = offa | (tail ? dropa : 0u), vb = offb | (tail ? dropb : 0u);
     // operand load i of the descriptor [base, base + bytes)
-    auto load = [&](const uint8_t* base, uint32_t bytes, int i, uint32_t lds, auto nt) {
-      const uint32_t v = off[ONE ? 0 : i] | ((d << (31 - (ONE ? 0 : i))) & 0x80000000u);
-      const uint32_t skip = ONE ? i * hop : 0;
-      const int rest = (int)bytes - (int)skip;         // signed: a scalar maximum
-      const __amdgpu_buffer_rsrc_t r = rsrc(base + skip, (uint32_t)(rest > 0 ? rest : 0));
+    auto load = [&](const uint8_t* base, uint32_t bytes, uint32_t v, int i, uint32_t lds, auto nt) {
+      const int rest = (int)bytes - (int)(i * hop);         // signed: a scalar maximum
+      const __amdgpu_buffer_rsrc_t r = rsrc(base + i * hop, (uint32_t)(rest > 0 ? rest : 0));
       if constexpr (decltype(nt)::value) dma16nt(r, v, ko, lds + i * C::WAVES * 1024);
       else dma16(r, v, ko, lds + i * C::WAVES * 1024);
     };
 #pragma unroll
     for (int i = 0; i < BL; ++i)
-      if (part == i * parts / (AL + BL)) load(lo.b, lo.b_bytes, i, st + C::BM * 128, std::bool_constant<NT>());
+      if (part == i * parts / (AL + BL)) load(lo.b, lo.b_bytes, vb, i, st + C::BM * 128, std::bool_constant<NT>());
 #pragma unroll
     for (int i = 0; i < AL; ++i)
-      if (part == (BL + i) * parts / (AL + BL)) load(lo.a, lo.a_bytes, i, st, std::false_type());
+      if (part == (BL + i) * parts / (AL + BL)) load(lo.a, lo.a_bytes, va, i, st, std::false_type());
   };
   // Scales: waves 0 .. SW - 1 bring 64 rows of A each, wave SW the B blocks'.
   auto issue_scales = [&]() {
@@ -427,22 +432,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   // the accumulators of a pair are eight neighbouring columns of a lane:
   // row x of fragment j is column 32 (j / 2) + 8 (x / 4) + 4 (j % 2) + x % 4.
   const int x16 = lane & 15, q = lane >> 4;
-  uint32_t xa[2], xb[2];       // byte offsets of chunk q of fragments 0 and 1
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int ra = 16 * e + x16, rb = 8 * (x16 >> 2) + 4 * e + (x16 & 3);
-    xa[e] = (uint32_t)(ra * 128 + ((q ^ swz(wm * C::WTM + ra)) << 4));
-    xb[e] = (uint32_t)(rb * 128 + ((q ^ swz(wn * C::WTN + rb)) << 4));
-  }
+  const uint32_t xa = (uint32_t)(x16 * 128 + ((q ^ swz_a(x16)) << 4));       // byte offset of chunk q; ^ 64: of chunk 4 + q
+  const uint32_t xb = (uint32_t)((8 * (x16 >> 2) + (x16 & 3)) * 128 + ((q ^ swz_b(8 * (x16 >> 2) + (x16 & 3))) << 4));
   // A fragment's 32 codes of a lane; whole vectors throughout, so that they
   // stay in consecutive registers across the loop.
-  // fragment i: 16 i rows on, i / 2 flips the swizzle's bit 2 every 32 rows; chunk 4 + q is bit 2's other value
-  auto rd = [&](const uint8_t* base, const uint32_t (&xo)[2], int i) -> v8i {
-    const uint32_t o = xo[i & 1], flip = ((i >> 1) & 1) * 64u;
-    const uint8_t* r = base + (i >> 1) * 4096;
-    const v4i lo4 = *reinterpret_cast<const v4i*>(r + (o ^ flip));
-    const v4i hi4 = *reinterpret_cast<const v4i*>(r + (o ^ flip ^ 64u));
+  auto rd = [](const uint8_t* at, uint32_t xo) -> v8i {
+    const v4i lo4 = *reinterpret_cast<const v4i*>(at + xo), hi4 = *reinterpret_cast<const v4i*>(at + (xo ^ 64u));
     return __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto rd_a = [&](const uint8_t* stage_at, int i) { return rd(stage_at + wm * C::WTM * 128 + i * 2048, xa); };
+  auto rd_b = [&](const uint8_t* stage_at, int j) {
+    return rd(stage_at + C::BM * 128 + wn * C::WTN * 128 + (j >> 1) * 4096 + (j & 1) * 512, xb);
   };
 
   // Steps overlap: the last fragment row of a step multiplies after the barrier
@@ -467,13 +467,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
       acc[i][j][r] = __builtin_fmaf(tm[C::FAST ? 0 : i & 1][j][r], fi, acc[i][j][r]);
   };
   auto widen1 = [](const v8i& r, int e) -> v8h { return decode_fp8x8((uint32_t)r[2 * e], (uint32_t)r[2 * e + 1]); };
-  const uint32_t wa = wm * C::WTM * 128, wb = C::BM * 128 + wn * C::WTN * 128;
   // the first fragments of the current stage's step
   auto read_first = [&]() {
     const uint8_t* base = smem + stage * C::STAGE;
-    ra[0] = rd(base + wa, xa, 0);
+    ra[0] = rd_a(base, 0);
 #pragma unroll
-    for (int j = 0; j < FJ; ++j) rb[j] = rd(base + wb, xb, j);
+    for (int j = 0; j < FJ; ++j) rb[j] = rd_b(base, j);
     if constexpr (!C::FAST) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -513,7 +512,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     constexpr bool kHead = i == FI - 1;
     const uint8_t* base = smem + stage * C::STAGE;
     if constexpr (C::FAST) {
-      ra[(i + 1) & 1] = rd(base + wa, xa, kHead ? 0 : i + 1);
+      ra[(i + 1) & 1] = rd_a(base, kHead ? 0 : i + 1);
 #pragma unroll
       for (int j = 0; j < FJ; ++j) {
         constexpr int kBack = 2;       // added up this many fragments later
@@ -521,16 +520,16 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
         tm[0][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rb[j], ra[i & 1], v4f{}, 0, 0, 0, 0, 0, 0);
         if (!kHead && g < LS) issue(g, LS);
         fence();
-        if constexpr (kHead) rb[j] = rd(base + wb, xb, j);
+        if constexpr (kHead) rb[j] = rd_b(base, j);
         if (g >= kBack) add((g - kBack) / FJ, (g - kBack) % FJ, f[(g - kBack) / FJ]);
         else add(FI - 1, FJ - kBack + g, flast);
         fence();
       }
     } else {
-      ra[0] = rd(base + wa, xa, kHead ? 0 : i + 1);
+      ra[0] = rd_a(base, kHead ? 0 : i + 1);
       if constexpr (kHead) {
 #pragma unroll
-        for (int j = 0; j < FJ; ++j) rb[j] = rd(base + wb, xb, j);
+        for (int j = 0; j < FJ; ++j) rb[j] = rd_b(base, j);
       }
       fence();
 #pragma unroll
