@@ -628,46 +628,60 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     have = active;
 
     // ------------------------------------------------------------ epilogue
-    // lane: row x16 of each fragment row; a pair of fragments holds columns
-    // 32 jp + 8 q + 0 .. 7
+    // Through LDS, so that a store writes whole lines: a lane's accumulators
+    // are eight columns of one row (a pair of fragments holds columns 32 jp +
+    // 8 q + 0 .. 7), and stored from there each 16 lanes would touch 16 lines.  A
+    // wave puts kRows fragment rows at a time into its share of the stage that
+    // the next step's loads will fill (all of it has been read) and stores them
+    // row by row, 16 bytes a lane.
     if (active) {
+      constexpr int ES = OUT == kOutBf16 || OUT == kOutF16 ? 2 : 4;
+      constexpr int RB = C::WTN * ES, CH = RB / 16;            // bytes and 16-byte chunks of a wave tile's row
+      constexpr int kFit = C::STAGE / C::WAVES / (16 * RB), kRows = kFit >= 4 && FI % 4 == 0 ? 4 : (kFit >= 2 ? 2 : 1);
+      static_assert(kFit >= 1 && FI % kRows == 0, "a fragment row fits a wave's share of a stage");
       int ln = lane;                       // opaque: nothing below is kept through the K loop
       asm volatile("" : "+v"(ln));
       const int x16 = ln & 15, q = ln >> 4;
-      constexpr int ES = OUT == kOutBf16 || OUT == kOutF16 ? 2 : 4;
+      uint8_t* mine = smem + lstep * C::STAGE + w * (C::STAGE / C::WAVES);
+      auto slot = [](int row, int ch) { return row * RB + ((ch ^ (CH == 8 ? (row >> 1) & 7 : row & 15)) << 4); };
       const int64_t orow = (p.form == kGroupK ? (int64_t)t.g * p.rows : 0) + (int64_t)t.slice * p.rows;
-      int64_t row = t.row0 + wm * C::WTM + x16;
-      const int64_t n = t.n0 + wn * C::WTN + 8 * q;
+      const int lrow = ln / CH, ch = ln % CH;                  // a store instruction: 64 / CH rows
+      const int64_t row = t.row0 + wm * C::WTM + lrow, n = t.n0 + wn * C::WTN + ch * (16 / ES);
       uint8_t* dst = static_cast<uint8_t*>(p.out) + ((orow + row) * p.ldo + n) * ES;
+      const int64_t left = n < p.n ? t.row_end - row : 0;      // rows of the lane's column from here on
 #pragma unroll
-      for (int i = 0; i < FI; ++i) {
+      for (int i0 = 0; i0 < FI; i0 += kRows) {
 #pragma unroll
-        for (int jp = 0; jp < FJ / 2; ++jp) {
-          if (row < t.row_end && n + 32 * jp < p.n) {
-            const v4f lo4 = acc[i][2 * jp], hi4 = acc[i][2 * jp + 1];
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int jp = 0; jp < FJ / 2; ++jp) {
+            const v4f lo4 = acc[i0 + i][2 * jp], hi4 = acc[i0 + i][2 * jp + 1];
             if constexpr (ES == 2) {
               constexpr bool F16 = OUT == kOutF16;
-              reinterpret_cast<uint4*>(dst)[4 * jp] =
+              *reinterpret_cast<uint4*>(mine + slot(16 * i + x16, 4 * jp + q)) =
                   make_uint4(pack_half2<F16>(lo4[0], lo4[1]), pack_half2<F16>(lo4[2], lo4[3]),
                              pack_half2<F16>(hi4[0], hi4[1]), pack_half2<F16>(hi4[2], hi4[3]));
             } else {
-              v4f* d = reinterpret_cast<v4f*>(dst) + 8 * jp;
-              if constexpr (OUT == kOutF32Add) {
-                const v4f a0 = d[0], a1 = d[1];
-                d[0] = a0 + lo4;
-                d[1] = a1 + hi4;
-              } else {
-                d[0] = lo4;
-                d[1] = hi4;
-              }
+              *reinterpret_cast<v4f*>(mine + slot(16 * i + x16, 8 * jp + 2 * q)) = lo4;
+              *reinterpret_cast<v4f*>(mine + slot(16 * i + x16, 8 * jp + 2 * q + 1)) = hi4;
             }
           }
+        fence();
+#pragma unroll
+        for (int c = 0; c < 16 * kRows / (64 / CH); ++c) {
+          const int r = 16 * i0 + c * (64 / CH);               // the instruction's first row in the wave tile
+          v4f v = *reinterpret_cast<const v4f*>(mine + slot(c * (64 / CH) + lrow, ch));
+          if (r < left) {
+            v4f* d = reinterpret_cast<v4f*>(dst + r * p.ldo * ES);
+            if constexpr (OUT == kOutF32Add) v = *d + v;
+            *d = v;
+          }
         }
-        row += 16;
-        dst += 16 * p.ldo * ES;
         fence();
       }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    bar();                // every wave is done with that stage
     if (tile_at(++round) >= last) break;
     plan(round + ST - 1);
     t = tile_of(round);
