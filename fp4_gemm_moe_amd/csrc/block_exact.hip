@@ -4,13 +4,13 @@
 
 namespace hq {
 
-hipError_t launch_block_exact(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, bool nt) {
+hipError_t launch_block_exact(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, int policy) {
   using namespace blk;
   if (tile == kTile128x128)
-    return launch_out<Cfg<128, 128, 2, 2, 4, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, nt);
+    return launch_out<Cfg<128, 128, 2, 2, 4, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, policy);
   if (tile == kTile256x128)
-    return launch_out<Cfg<256, 128, 4, 2, 2, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, nt);
-  return launch_out<Cfg<64, 128, 2, 2, 5, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, nt);
+    return launch_out<Cfg<256, 128, 4, 2, 2, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, policy);
+  return launch_out<Cfg<64, 128, 2, 2, 5, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, policy);
 }
 
 }  // namespace hq

@@ -5,13 +5,13 @@
 
 namespace hq {
 
-hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, bool nt) {
+hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, int policy) {
   using namespace blk;
   switch (tile) {
-    case kTile256x256: return launch_out<Cfg<256, 256, 2, 4, 2, true>, kOutBf16, kOutF32>(s, p, dev, nt);
-    case kTile128x256: return launch_out<Cfg<128, 256, 2, 4, 3, true>, kOutBf16, kOutF32>(s, p, dev, nt);
-    case kTile128x128: return launch_out<Cfg<128, 128, 2, 2, 4, true>, kOutBf16, kOutF32>(s, p, dev, nt);
-    default: return launch_out<Cfg<64, 128, 2, 2, 5, true>, kOutBf16, kOutF32>(s, p, dev, nt);
+    case kTile256x256: return launch_out<Cfg<256, 256, 2, 4, 2, true>, kOutBf16, kOutF32>(s, p, dev, policy);
+    case kTile128x256: return launch_out<Cfg<128, 256, 2, 4, 3, true>, kOutBf16, kOutF32>(s, p, dev, policy);
+    case kTile128x128: return launch_out<Cfg<128, 128, 2, 2, 4, true>, kOutBf16, kOutF32>(s, p, dev, policy);
+    default: return launch_out<Cfg<64, 128, 2, 2, 5, true>, kOutBf16, kOutF32>(s, p, dev, policy);
   }
 }
 

@@ -207,9 +207,16 @@ hipError_t launch_tiled(hipStream_t s, BlockGemmArgs p, const DeviceInfo& dev, b
     p.out_kind = kOutF32;
     p.ldo = p.n;
   }
-  // weights that one m-tile reads once, by all compute units at once
-  const bool nt = p.form == kMasked && p.slot_rows <= 256;
-  const hipError_t e = fast ? launch_block_fast(s, p, dev, pl.tile, nt) : launch_block_exact(s, p, dev, pl.tile, nt);
+  // Results that the L2s cannot hold leave past them, and the operands stay
+  // (4096x17408x5120 371 -> 357 us, FP32 K-grouped 971 -> 925 us); partial sums
+  // and smaller results are read again soon.  Masked slots of at most 256 rows
+  // read each weight once, by all compute units at once: those loads stream too
+  // (64 slots of 256 rows, 4096x7168: 513 -> 473 us).
+  const int64_t bytes = (p.form == kGroupK ? p.groups : 1) * p.rows * p.n * (p.out_kind >= kOutF32 ? 4 : 2);
+  const int policy = p.form == kMasked && p.slot_rows <= 256               ? kPolStreamAll
+                     : pl.slices == 1 && bytes > (int64_t)32 << 20 ? kPolStreamOut
+                                                                           : kPolKeep;
+  const hipError_t e = fast ? launch_block_fast(s, p, dev, pl.tile, policy) : launch_block_exact(s, p, dev, pl.tile, policy);
   if (e != hipSuccess || pl.slices == 1) return e;
   const int64_t quads = p.rows * p.n / 4;
   hipLaunchKernelGGL(block_reduce, dim3((unsigned)up(quads, kReduceThreads)), dim3(kReduceThreads), 0, s,

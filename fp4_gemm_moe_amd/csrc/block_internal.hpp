@@ -14,6 +14,10 @@ enum BlockOut : int32_t { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutF32Add = 3
 // GroupForm's forms, and the product that sums over the groups' K ranges.
 constexpr int32_t kGroupK = 3;
 
+// Which accesses of a tiled launch take the non-temporal policy: none, the
+// stores of results, or those and the loads of b.
+enum BlockPolicy : int32_t { kPolKeep = 0, kPolStreamOut = 1, kPolStreamAll = 2 };
+
 // out[r, n] = sum over K blocks of sa[r, kb] sb[n / 128, kb] (a[r] . b[n])_kb,
 // in one of the forms of GroupForm or kGroupK.
 struct BlockGemmArgs {

@@ -11,8 +11,8 @@ namespace hq {
 // Tile shapes of the tiled kernel (rows x columns).
 enum BlockTile : int { kTile256x256, kTile256x128, kTile128x256, kTile128x128, kTile64x128 };
 
-hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, bool nt);
-hipError_t launch_block_exact(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, bool nt);
+hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, int policy);
+hipError_t launch_block_exact(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, int policy);
 
 namespace blk {
 
@@ -27,13 +27,13 @@ int64_t tile_count(const BlockGemmArgs& p) {
   return (p.rows / C::BM + p.groups) * nt;
 }
 
-template <class C, int OUT, bool NT>
+template <class C, int OUT, int POL>
 hipError_t launch_one(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev) {
   // the dynamic-LDS attribute, once per device (setting it twice is harmless)
   static std::atomic<bool> set[64];
   const bool cached = dev.device >= 0 && dev.device < 64;
   if (!cached || !set[dev.device].load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute((const void*)block_gemm_tiled<C, OUT, NT>,
+    const hipError_t e = hipFuncSetAttribute((const void*)block_gemm_tiled<C, OUT, POL>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != hipSuccess) return e;
     if (cached) set[dev.device].store(true, std::memory_order_release);
@@ -41,18 +41,21 @@ hipError_t launch_one(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& d
   // one workgroup per compute unit; whole eighths, one for each XCD
   int64_t grid = (tile_count<C>(p) + 7) / 8 * 8;
   if (grid > dev.num_cus) grid = dev.num_cus;
-  hipLaunchKernelGGL((block_gemm_tiled<C, OUT, NT>), dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, p);
+  hipLaunchKernelGGL((block_gemm_tiled<C, OUT, POL>), dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, s, p);
   return hipGetLastError();
 }
 
-// The instantiation for p's output among OUTS.
+// The instantiation for the policy, and for p's output among OUTS.
+template <class C, int OUT>
+hipError_t launch_policy(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int policy) {
+  if (policy == kPolStreamAll) return launch_one<C, OUT, kPolStreamAll>(s, p, dev);
+  if (policy == kPolStreamOut) return launch_one<C, OUT, kPolStreamOut>(s, p, dev);
+  return launch_one<C, OUT, kPolKeep>(s, p, dev);
+}
 template <class C, int... OUTS>
-hipError_t launch_out(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, bool nt) {
+hipError_t launch_out(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int policy) {
   hipError_t e = hipErrorInvalidValue;
-  (void)((p.out_kind == OUTS
-              ? (e = nt ? launch_one<C, OUTS, true>(s, p, dev) : launch_one<C, OUTS, false>(s, p, dev), true)
-              : false) ||
-         ...);
+  (void)((p.out_kind == OUTS ? (e = launch_policy<C, OUTS>(s, p, dev, policy), true) : false) || ...);
   return e;
 }
 

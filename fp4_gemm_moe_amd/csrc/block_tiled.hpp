@@ -249,9 +249,8 @@ __device__ __forceinline__ Operands operands(const BlockGemmArgs& p, const Tile&
   return o;
 }
 
-// OUT: BlockOut of the stores (a K split stores FP32 partials).  NT: B's loads
-// take the non-temporal policy.
-template <class C, int OUT, bool NT>
+// OUT: BlockOut of the stores (a K split stores FP32 partials).  POL: BlockPolicy.
+template <class C, int OUT, int POL>
 __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs p) {
   constexpr int FI = C::FI, FJ = C::FJ, ST = C::ST, AL = C::AL, BL = C::BL;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -369,7 +368,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     };
 #pragma unroll
     for (int i = 0; i < BL; ++i)
-      if (part == i * parts / (AL + BL)) load(lo.b, lo.b_bytes, vb, i, st + C::BM * 128, std::bool_constant<NT>());
+      if (part == i * parts / (AL + BL)) load(lo.b, lo.b_bytes, vb, i, st + C::BM * 128, std::bool_constant<POL == kPolStreamAll>());
 #pragma unroll
     for (int i = 0; i < AL; ++i)
       if (part == (BL + i) * parts / (AL + BL)) load(lo.a, lo.a_bytes, va, i, st, std::false_type());
@@ -674,7 +673,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
           if (r < left) {
             v4f* d = reinterpret_cast<v4f*>(dst + r * p.ldo * ES);
             if constexpr (OUT == kOutF32Add) v = *d + v;
-            *d = v;
+            if constexpr (POL != kPolKeep) __builtin_nontemporal_store(v, d);
+            else *d = v;
           }
         }
         fence();
