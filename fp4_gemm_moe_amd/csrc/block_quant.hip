@@ -17,7 +17,7 @@ constexpr int kThreads = 256;
 // store of codes, and an amax over the lane octet in three DPP steps.
 // Octets are numbered along the whole tensor, so any k (a multiple of 32)
 // keeps every lane busy but those past a row's last partial block.
-template <bool F16, bool SWIGLU>
+template <bool F16, bool SWIGLU, bool NT>
 __global__ __launch_bounds__(kThreads) void block_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t k,
                                                               int32_t nkb, const int32_t* __restrict__ last_end,
                                                               uint8_t* __restrict__ q, float* __restrict__ sf) {
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(kThreads) void block_rows_kernel(const uint16_t* __
   if (!in) return;
   uint32_t w[4];
   block_codes(f, s, w);
-  *reinterpret_cast<uint4*>(q + row * k + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  store16<NT>(q + row * k + c, u32x4{w[0], w[1], w[2], w[3]});
   if (l == 0) sf[row * nkb + kb] = s;
 }
 
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kThreads) void block_rows_kernel(const uint16_t* __
 //   TRANS = false: one scale per tile (128 x 128 blocks), codes in x's layout.
 //   TRANS = true: the codes go through LDS and leave as rows of q [k, m]; the
 //   scale is per tile (TWO_D) or per column of x (1 x 128 blocks of q's rows).
-template <bool F16, bool TWO_D, bool TRANS>
+template <bool F16, bool TWO_D, bool TRANS, bool NT>
 __global__ __launch_bounds__(kThreads) void block_tile_kernel(const uint16_t* __restrict__ x, int64_t m, int64_t k,
                                                               int32_t tiles_m, int32_t tiles_k,
                                                               uint8_t* __restrict__ q, float* __restrict__ sf) {
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void block_tile_kernel(const uint16_t* __
         unpack16<F16>(v[p][0], v[p][1], f);
         uint32_t o[4];
         block_codes(f, s, o);
-        *reinterpret_cast<uint4*>(qb + r * k + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        store16<NT>(qb + r * k + c, u32x4{o[0], o[1], o[2], o[3]});
       }
     }
     if (tid == 0) sf[(bt * tiles_m + tm) * tiles_k + tk] = s;
@@ -191,55 +191,56 @@ __global__ __launch_bounds__(kThreads) void block_tile_kernel(const uint16_t* __
     for (int p = 0; p < 4; ++p) {
       const int cc = 32 * p + r8;
       if (k0 + cc < k && m0 + 16 * l < m)
-        *reinterpret_cast<uint4*>(qb + (k0 + cc) * m + m0 + 16 * l) =
-            *reinterpret_cast<const uint4*>(lt + cc * 36 + 4 * l);
+        store16<NT>(qb + (k0 + cc) * m + m0 + 16 * l, *reinterpret_cast<const u32x4*>(lt + cc * 36 + 4 * l));
     }
   }
+}
+
+template <bool SWIGLU>
+hipError_t launch_rows(hipStream_t s, const uint16_t* x, int64_t rows, int64_t k, const int32_t* last_end, uint8_t* q,
+                       float* sf, bool fp16) {
+  const int64_t nkb = (k + 127) / 128, blocks = (rows * nkb + kThreads / 8 - 1) / (kThreads / 8);
+  const bool nt = rows * k > kStreamBytes;
+#define HQ_ROWS(F, N)                                                                                                \
+  hipLaunchKernelGGL((block_rows_kernel<F, SWIGLU, N>), dim3((unsigned)blocks), dim3(kThreads), 0, s, x, rows, k,   \
+                     (int32_t)nkb, last_end, q, sf)
+  if (fp16 && nt) HQ_ROWS(true, true);
+  else if (fp16) HQ_ROWS(true, false);
+  else if (nt) HQ_ROWS(false, true);
+  else HQ_ROWS(false, false);
+#undef HQ_ROWS
+  return hipGetLastError();
+}
+
+template <bool TWO_D, bool TRANS>
+hipError_t launch_tiles(hipStream_t s, const uint16_t* x, int64_t batch, int64_t m, int64_t k, uint8_t* q, float* sf,
+                        bool fp16) {
+  const int64_t tk = (k + 127) / 128, tm = (m + 127) / 128;
+  const bool nt = batch * m * k > kStreamBytes;
+#define HQ_TILE(F, N)                                                                                          \
+  hipLaunchKernelGGL((block_tile_kernel<F, TWO_D, TRANS, N>), dim3((unsigned)(batch * tm * tk)), dim3(kThreads), 0, \
+                     s, x, m, k, (int32_t)tm, (int32_t)tk, q, sf)
+  if (fp16 && nt) HQ_TILE(true, true);
+  else if (fp16) HQ_TILE(true, false);
+  else if (nt) HQ_TILE(false, true);
+  else HQ_TILE(false, false);
+#undef HQ_TILE
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_block_quant(hipStream_t s, const uint16_t* x, int64_t batch, int64_t m, int64_t k, uint8_t* q,
                               float* sf, bool two_d, bool transpose, bool fp16) {
-  const int64_t tk = (k + 127) / 128, tm = (m + 127) / 128;
-  if (!two_d && !transpose) {
-    const int64_t rows = batch * m;
-    const int64_t blocks = (rows * tk + kThreads / 8 - 1) / (kThreads / 8);
-    if (fp16)
-      hipLaunchKernelGGL((block_rows_kernel<true, false>), dim3((unsigned)blocks), dim3(kThreads), 0, s, x, rows, k,
-                         (int32_t)tk, (const int32_t*)nullptr, q, sf);
-    else
-      hipLaunchKernelGGL((block_rows_kernel<false, false>), dim3((unsigned)blocks), dim3(kThreads), 0, s, x, rows, k,
-                         (int32_t)tk, (const int32_t*)nullptr, q, sf);
-    return hipGetLastError();
-  }
-  const dim3 grid((unsigned)(batch * tm * tk));
-#define HQ_TILE(F, D, T)                                                                                   \
-  hipLaunchKernelGGL((block_tile_kernel<F, D, T>), grid, dim3(kThreads), 0, s, x, m, k, (int32_t)tm, (int32_t)tk, q, sf)
-  if (fp16) {
-    if (two_d && transpose) HQ_TILE(true, true, true);
-    else if (two_d) HQ_TILE(true, true, false);
-    else HQ_TILE(true, false, true);
-  } else {
-    if (two_d && transpose) HQ_TILE(false, true, true);
-    else if (two_d) HQ_TILE(false, true, false);
-    else HQ_TILE(false, false, true);
-  }
-#undef HQ_TILE
-  return hipGetLastError();
+  if (two_d && transpose) return launch_tiles<true, true>(s, x, batch, m, k, q, sf, fp16);
+  if (two_d) return launch_tiles<true, false>(s, x, batch, m, k, q, sf, fp16);
+  if (transpose) return launch_tiles<false, true>(s, x, batch, m, k, q, sf, fp16);
+  return launch_rows<false>(s, x, batch * m, k, nullptr, q, sf, fp16);
 }
 
 hipError_t launch_swiglu_block_quant(hipStream_t s, const uint16_t* x, int64_t rows, int64_t h,
                                      const int32_t* last_end, uint8_t* q, float* sf, bool fp16) {
-  const int64_t nkb = (h + 127) / 128;
-  const int64_t blocks = (rows * nkb + kThreads / 8 - 1) / (kThreads / 8);
-  if (fp16)
-    hipLaunchKernelGGL((block_rows_kernel<true, true>), dim3((unsigned)blocks), dim3(kThreads), 0, s, x, rows, h,
-                       (int32_t)nkb, last_end, q, sf);
-  else
-    hipLaunchKernelGGL((block_rows_kernel<false, true>), dim3((unsigned)blocks), dim3(kThreads), 0, s, x, rows, h,
-                       (int32_t)nkb, last_end, q, sf);
-  return hipGetLastError();
+  return launch_rows<true>(s, x, rows, h, last_end, q, sf, fp16);
 }
 
 }  // namespace hq

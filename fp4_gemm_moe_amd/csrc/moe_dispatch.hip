@@ -308,52 +308,64 @@ __global__ __launch_bounds__(kThreads) void combine_rows(const uint16_t* __restr
 }
 
 // dy[row] = weights[t, j] dout[t] and dweights[t, j] = dout[t] . y[row], the
-// product summed in FP32.  One workgroup takes a token: a thread's share of
-// dout is read per slot from the nearest cache, the dot product is reduced
-// over the wave and then over the four waves in a fixed order.
-template <bool F16>
-__global__ __launch_bounds__(kThreads) void combine_bwd(const uint16_t* __restrict__ dout,
-                                                        const uint16_t* __restrict__ y, int64_t tokens, int64_t h,
-                                                        const int32_t* __restrict__ row_map, int32_t topk,
-                                                        const float* __restrict__ weights, PadRows pad,
-                                                        int64_t max_rows, uint16_t* __restrict__ dy,
-                                                        float* __restrict__ dweights) {
-  __shared__ float part[64][4];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+// product summed in FP32.  One workgroup takes a token, each of its waves (up
+// to eight) a slot at a time: a lane's share of the row, 16 bytes of every
+// kilobyte, four loads in flight, then one reduction over the wave in a fixed
+// order.  dout's row comes from memory once and from a cache for the other
+// waves.  The bytes of y and dy bound it; with few tokens the chain of loads
+// behind a slot does, and a wave a slot keeps that chain one row long.
+template <bool F16, bool NT>
+__global__ __launch_bounds__(512) void combine_bwd(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y,
+                                                   int64_t tokens, int64_t h, const int32_t* __restrict__ row_map,
+                                                   int32_t topk, const float* __restrict__ weights, PadRows pad,
+                                                   int64_t max_rows, uint16_t* __restrict__ dy,
+                                                   float* __restrict__ dweights) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, waves = blockDim.x >> 6;
+  const int64_t chunks = h / 8;
   if ((int64_t)blockIdx.x >= tokens) {
     const int g = (int)((blockIdx.x - tokens) / kPadParts), p = (int)((blockIdx.x - tokens) % kPadParts);
     int64_t r0, r1;
     pad_range(pad, g, max_rows, r0, r1);
-    for (int64_t r = r0 + p * 4 + w; r < r1; r += kPadParts * 4)
-      for (int64_t c = lane; c < h / 8; c += 64) reinterpret_cast<uint4*>(dy + r * h)[c] = make_uint4(0, 0, 0, 0);
+    for (int64_t r = r0 + p * waves + w; r < r1; r += kPadParts * waves)
+      for (int64_t c = lane; c < chunks; c += 64) store16<NT>(dy + r * h + 8 * c, u32x4{0, 0, 0, 0});
     return;
   }
   const int64_t t = blockIdx.x;
-  for (int j = 0; j < topk; ++j) {
+  const uint4* dt = reinterpret_cast<const uint4*>(dout + t * h);
+  for (int j = w; j < topk; j += waves) {
     const int32_t r = row_map[t * topk + j];
     float dot = 0.0f;
     if (r >= 0 && r < max_rows) {
       const float wt = weights[t * topk + j];
-      for (int64_t c = tid; c < h / 8; c += kThreads) {
-        const uint4 dv = reinterpret_cast<const uint4*>(dout + t * h)[c];
-        const uint4 yv = load_nt(reinterpret_cast<const uint4*>(y + (int64_t)r * h) + c);
-        const uint32_t d[4] = {dv.x, dv.y, dv.z, dv.w}, v[4] = {yv.x, yv.y, yv.z, yv.w};
-        uint32_t o[4];
+      const uint4* yr = reinterpret_cast<const uint4*>(y + (int64_t)r * h);
+      uint16_t* out = dy + (int64_t)r * h;
+      for (int64_t c0 = lane; c0 < chunks; c0 += 256) {
+        uint4 dv[4], yv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = half_lo<F16>(d[i]), b = half_hi<F16>(d[i]);
-          dot = __builtin_fmaf(a, half_lo<F16>(v[i]), dot);
-          dot = __builtin_fmaf(b, half_hi<F16>(v[i]), dot);
-          o[i] = pack_half2<F16>(wt * a, wt * b);
+        for (int u = 0; u < 4; ++u)
+          if (c0 + 64 * u < chunks) {
+            dv[u] = dt[c0 + 64 * u];
+            yv[u] = load_nt(yr + c0 + 64 * u);
+          }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (c0 + 64 * u >= chunks) continue;
+          const uint32_t d[4] = {dv[u].x, dv[u].y, dv[u].z, dv[u].w}, v[4] = {yv[u].x, yv[u].y, yv[u].z, yv[u].w};
+          u32x4 o;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = half_lo<F16>(d[i]), b = half_hi<F16>(d[i]);
+            dot = __builtin_fmaf(a, half_lo<F16>(v[i]), dot);
+            dot = __builtin_fmaf(b, half_hi<F16>(v[i]), dot);
+            o[i] = pack_half2<F16>(wt * a, wt * b);
+          }
+          store16<NT>(out + 8 * (c0 + 64 * u), o);
         }
-        reinterpret_cast<uint4*>(dy + (int64_t)r * h)[c] = make_uint4(o[0], o[1], o[2], o[3]);
       }
+      for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
     }
-    for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 64);
-    if (lane == 0) part[j][w] = dot;
+    if (lane == 0) dweights[t * topk + j] = dot;
   }
-  __syncthreads();
-  if (tid < topk) dweights[t * topk + tid] = ((part[tid][0] + part[tid][1]) + part[tid][2]) + part[tid][3];
 }
 
 }  // namespace
@@ -431,12 +443,16 @@ hipError_t launch_moe_combine_backward(hipStream_t s, const uint16_t* dout, cons
                                        PadRows pad, int64_t max_rows, uint16_t* dy, float* dweights, bool fp16) {
   const int64_t blocks = tokens + pad_blocks(pad);
   if (blocks == 0) return hipSuccess;
-  if (fp16)
-    hipLaunchKernelGGL(combine_bwd<true>, dim3((unsigned)blocks), dim3(kThreads), 0, s, dout, y, tokens, h, row_map,
-                       topk, weights, pad, max_rows, dy, dweights);
-  else
-    hipLaunchKernelGGL(combine_bwd<false>, dim3((unsigned)blocks), dim3(kThreads), 0, s, dout, y, tokens, h, row_map,
-                       topk, weights, pad, max_rows, dy, dweights);
+  const int waves = topk > 8 ? 8 : (topk < 4 ? 4 : topk);      // four at least, for the padding rows
+  const bool nt = max_rows * h * 2 > kStreamBytes;
+#define HQ_BWD(F, N)                                                                                               \
+  hipLaunchKernelGGL((combine_bwd<F, N>), dim3((unsigned)blocks), dim3(64 * waves), 0, s, dout, y, tokens, h, row_map, \
+                     topk, weights, pad, max_rows, dy, dweights)
+  if (fp16 && nt) HQ_BWD(true, true);
+  else if (fp16) HQ_BWD(true, false);
+  else if (nt) HQ_BWD(false, true);
+  else HQ_BWD(false, false);
+#undef HQ_BWD
   return hipGetLastError();
 }
 
