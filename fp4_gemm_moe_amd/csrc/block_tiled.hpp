@@ -314,9 +314,11 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     }
     if (lane == 0) ring[round % kRing] = u;
   };
+  // With one step a tile, the loads' cursor ends a step of round r at round r +
+  // ST: the rounds up to there are planned.
   static_assert(ST + 2 <= kRing, "tiles in flight");
 #pragma unroll 1
-  for (int r = 0; r < ST; ++r) plan(r);
+  for (int r = 0; r <= ST; ++r) plan(r);
   auto upcoming = [&](int round) -> Operands {
     const Operands& v = ring[round % kRing].o;
     Operands o;
@@ -683,7 +685,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     bar();                // every wave is done with that stage
     if (tile_at(++round) >= last) break;
-    plan(round + ST - 1);
+    plan(round + ST);
     t = tile_of(round);
     clear();
   }

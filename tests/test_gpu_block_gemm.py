@@ -283,3 +283,38 @@ def test_repeats_are_bit_identical_and_run_on_another_stream():
         torch.cuda.synchronize()
         outs.append(out)
     assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_tiles_of_one_step(dtype):
+    """More tiles than compute units, each a single K block (some none): the loads
+    run several tiles ahead of the sums."""
+    what = f"one-step tiles {dtype}"
+    U.banner(what)
+    r = H.rng("one step")
+    blocks = [1, 0, 1, 1, 0, 1] * 8
+    E, m, n, K = len(blocks), 600, 1104, 128 * sum(blocks)
+    ends = 128 * np.cumsum(blocks)
+    (a, sa), (b, sb) = H.codes(r, m, K), H.codes(r, n, K, True)
+    out = torch.full((E, m, n), float("nan"), dtype=dtype, device="cuda")
+    hq.hq_block_group_k_gemm(H.dev(a), H.dev(sa), H.dev(b), H.dev(sb), U.dev_i32(ends, "cuda"), out)
+    for g in range(E):
+        lo, hi = int(ends[g]) - 128 * blocks[g], int(ends[g])
+        ref, mag = B.gemm(a[:, lo:hi], sa[:, lo // 128:hi // 128], b[:, lo:hi], sb[:, lo // 128:hi // 128])
+        # the FP8 matrix instructions' own bound on a sum of one block (BF16 results):
+        # each group of eight products keeps 13 bits below its largest, so it
+        # loses less than 8 x 2^-13 of that
+        own = 2.0 ** -10 * mag if dtype is BF16 else 0.0
+        H.check(out[g], ref, H.product_bound(ref, mag, 128, dtype) + own, f"{what} group {g}")
+    # short rows through the dense and contiguous forms
+    m, n, k = 1500, 2056, 96
+    (a, sa), (b, sb) = H.codes(r, m, k), H.codes(r, n, k, True)
+    ref, mag = B.gemm(a, sa, b, sb)
+    for grouped in (False, True):
+        out = torch.empty((m, n), dtype=dtype, device="cuda")
+        if grouped:
+            hq.hq_block_group_contiguous_gemm(H.dev(a), H.dev(sa), H.dev(b[None]), H.dev(sb[None]),
+                                              U.dev_i32([m], "cuda"), out)
+        else:
+            hq.hq_block_gemm(H.dev(a), H.dev(sa), H.dev(b), H.dev(sb), out)
+        H.check(out, ref, H.product_bound(ref, mag, k, dtype), f"{what} grouped={grouped}")
