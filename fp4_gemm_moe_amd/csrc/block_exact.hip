@@ -9,7 +9,7 @@ hipError_t launch_block_exact(hipStream_t s, const BlockGemmArgs& p, const Devic
   if (tile == kTile128x128)
     return launch_out<Cfg<128, 128, 2, 2, 4, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, policy);
   if (tile == kTile256x128)
-    return launch_out<Cfg<256, 128, 4, 2, 2, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, policy);
+    return launch_out<Cfg<256, 128, 4, 2, 3, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, policy);
   return launch_out<Cfg<64, 128, 2, 2, 5, false>, kOutBf16, kOutF16, kOutF32, kOutF32Add>(s, p, dev, policy);
 }
 

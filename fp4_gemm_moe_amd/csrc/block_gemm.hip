@@ -123,7 +123,7 @@ struct Shape {
 };
 constexpr Shape kFast[] = {{kTile256x256, 256, 256, 2.13}, {kTile128x256, 128, 256, 1.30},
                            {kTile128x128, 128, 128, 0.80}, {kTile64x128, 64, 128, 0.65}};
-constexpr Shape kExact[] = {{kTile256x128, 256, 128, 2.60}, {kTile128x128, 128, 128, 1.40}, {kTile64x128, 64, 128, 0.90}};
+constexpr Shape kExact[] = {{kTile256x128, 256, 128, 1.95}, {kTile128x128, 128, 128, 1.40}, {kTile64x128, 64, 128, 0.90}};
 
 constexpr double kBytesPerUs = 5.0e6;      // HBM, of the partial sums and of weights that are read once
 constexpr double kLaunchUs = 3.0;          // a further launch on the stream
@@ -146,7 +146,6 @@ Plan plan_uniform(const BlockGemmArgs& p, int64_t n, const DeviceInfo& dev, bool
   Plan best;
   const int64_t cus = dev.num_cus;
   auto consider = [&](const Shape& sh) {
-    if (sh.tile != kTile64x128 && p.nkb < 4) return;      // they fetch four K blocks' scales at a time
     const int64_t mt = up(p.slot_rows, sh.bm), tiles = mt * p.groups * up(n, sh.bn);
     for (int s = 1; s <= 16 && (s == 1 || s * 4 <= p.nkb); ++s) {
       Plan c;
@@ -191,7 +190,7 @@ Plans plan_all(const BlockGemmArgs& p, const DeviceInfo& dev, bool fast, uint64_
 // deeper stages of the smaller tiles serve better; many share each weight tile.
 int plan_grouped(const BlockGemmArgs& p, bool fast) {
   const int64_t per = p.form == kContiguous ? up(p.rows, p.groups) : (p.form == kGroupK ? p.rows : p.slot_rows);
-  if (p.nkb < 4 || per <= 32) return kTile64x128;
+  if (per <= 32) return kTile64x128;
   if (!fast) return per <= 128 ? kTile128x128 : kTile256x128;
   const int64_t limit = p.form == kContiguous ? 1024 : 128;
   return per <= limit ? kTile128x256 : kTile256x256;
