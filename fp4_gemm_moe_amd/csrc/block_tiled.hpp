@@ -101,6 +101,8 @@ struct Cfg {
   // four K blocks in a row of the operand.  Otherwise each step brings its own
   // dword per row.
   static constexpr bool GROUPED = ST == 2;
+  // Two stages: they are refilled in halves (HALF below).
+  static constexpr bool HALF = ST == 2;
   static constexpr int SBUF = GROUPED ? BM * 16 + 1024 : BM * 4 + 256;
   static constexpr int SBUFS = GROUPED ? 2 : ST;
   static constexpr int SMEM = ST * STAGE + SBUFS * SBUF;
@@ -108,6 +110,7 @@ struct Cfg {
   static_assert(WTM % 32 == 0 && WTN == 64 && BN % 128 == 0, "wave tiles");
   static_assert(AL >= 1 && BL >= 1 && BM / 8 % WAVES == 0 && BN / 8 % WAVES == 0, "whole loads");
   static_assert(BM % 64 == 0 && SW + 1 <= WAVES, "scale loads");
+  static_assert(!HALF || (WTM == 16 * WAVES && FI == 8), "a load of A covers half of the fragment rows of one row of waves");
 };
 
 struct Table {
@@ -354,8 +357,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     lkb0 = t.kb0;
     lnk = t.nk;
   }
-  // issues part `part` of `parts` of the cursor's step; bit 31 of an offset drops the load
-  auto issue = [&](int part, int parts) {
+  // issues part `part` of `parts` of the cursor's step's loads first .. first +
+  // count - 1, B's and then A's (HALF: A's even ones, then its odd ones); bit 31
+  // of an offset drops the load
+  auto issue = [&](int part, int parts, int first, int count) {
     const int kb = lkb0 + lk;
     const uint32_t st = lds0 + (uint32_t)lstep * C::STAGE + (uint32_t)w * 1024;
     const uint32_t ko = (uint32_t)kb * 128;
@@ -369,11 +374,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
       else dma16(r, v, ko, lds + i * C::WAVES * 1024);
     };
 #pragma unroll
-    for (int i = 0; i < BL; ++i)
-      if (part == i * parts / (AL + BL)) load(lo.b, lo.b_bytes, vb, i, st + C::BM * 128, std::bool_constant<POL == kPolStreamAll>());
-#pragma unroll
-    for (int i = 0; i < AL; ++i)
-      if (part == (BL + i) * parts / (AL + BL)) load(lo.a, lo.a_bytes, va, i, st, std::false_type());
+    for (int l = 0; l < AL + BL; ++l) {
+      if (l < first || l >= first + count || part != (l - first) * parts / count) continue;
+      const int i = l < BL ? l : !C::HALF ? l - BL : (l - BL) * 2 < AL ? (l - BL) * 2 : (l - BL) * 2 - AL + 1;
+      if (l < BL) load(lo.b, lo.b_bytes, vb, i, st + C::BM * 128, std::bool_constant<POL == kPolStreamAll>());
+      else load(lo.a, lo.a_bytes, va, i, st, std::false_type());
+    }
   };
   // Scales: waves 0 .. SW - 1 bring 64 rows of A each, wave SW the B blocks'.
   auto issue_scales = [&]() {
@@ -405,21 +411,43 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   auto issue_all = [&]() {
     issue_scales();
 #pragma unroll
-    for (int s = 0; s < AL + BL; ++s) issue(s, AL + BL);
+    for (int s = 0; s < AL + BL; ++s) issue(s, AL + BL, 0, AL + BL);
   };
   // vector-memory operations of a step per wave, where that is the same for every step
   constexpr int kOps = AL + BL;
-#pragma unroll 1
-  for (int s = 0; s < ST - 1; ++s) {
-    issue_all();
+  // HALF: a stage is refilled in two halves.  Its early loads are B and the A
+  // rows of the first half of the fragment rows, its late ones the rest of A.
+  // When a step has read its first half (B's fragments stay in registers) a
+  // barrier in its middle frees that half, and the early loads of the step after
+  // next go there; the late ones follow at the start of the next step.  Each
+  // half has a step and a half to land: it is waited for where it is first read,
+  // at the end of the step before (early) or in the middle of its own (late),
+  // with one younger half step of each kind, kOps operations, in flight.
+  constexpr int kEarly = BL + AL / 2, kLate = AL - AL / 2;
+  auto issue_early = [&]() {
+    issue_scales();
+#pragma unroll
+    for (int s = 0; s < kEarly; ++s) issue(s, kEarly, 0, kEarly);
+  };
+  if constexpr (C::HALF) {
+    issue_early();
+#pragma unroll
+    for (int s = 0; s < kLate; ++s) issue(s, kLate, kEarly, kLate);
     advance();
+    issue_early();
+  } else {
+#pragma unroll 1
+    for (int s = 0; s < ST - 1; ++s) {
+      issue_all();
+      advance();
+    }
   }
   // waits until the next step's loads have landed: the operations of the ST - 2
-  // steps after it may stay in flight (with two stages nothing may).  Memory
+  // steps after it may stay in flight.  Memory
   // operations retire in the order of issue, so later stores only make the
   // wait stricter.
   auto land = [&]() {
-    if constexpr (ST == 2) wait_vm<0>();
+    if constexpr (C::HALF) wait_vm<kOps>();      // scales and stores among them make the wait stricter
     else if (w <= C::SW) wait_vm<(ST - 2) * (kOps + 1)>();
     else wait_vm<(ST - 2) * kOps>();
     bar();
@@ -455,6 +483,15 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   int stage = 0, group = 0;
   constexpr int G = FI * FJ, GB = G - FJ;     // fragments of a step, of its body
   constexpr int LS = GB < AL + BL ? GB : AL + BL;     // load slots, from the body's first fragment on
+  constexpr int kMid = FI / 2 - 1;            // HALF: the row before which a step's first half has been read
+  auto issue_at = [&](int g) {                // the loads of the body's fragment g
+    if constexpr (C::HALF) {
+      if (g < kLate) issue(g, kLate, kEarly, kLate);
+      else if (g >= kMid * FJ && g < kMid * FJ + kEarly) issue(g - kMid * FJ, kEarly, 0, kEarly);
+    } else if (g < LS) {
+      issue(g, LS, 0, AL + BL);
+    }
+  };
   auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
   constexpr int D = C::FAST ? 1 : 2;
   v4f tm[D][FJ];                // FAST: fragment g's sum, added up two fragments later; else a row's, added during the next
@@ -519,7 +556,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
         constexpr int kBack = 2;       // added up this many fragments later
         const int g = i * FJ + j;
         tm[0][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(rb[j], ra[i & 1], v4f{}, 0, 0, 0, 0, 0, 0);
-        if (!kHead && g < LS) issue(g, LS);
+        if (!kHead) issue_at(g);
         fence();
         if constexpr (kHead) rb[j] = rd_b(base, j);
         if (g >= kBack) add((g - kBack) / FJ, (g - kBack) % FJ, f[(g - kBack) / FJ]);
@@ -539,7 +576,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
         for (int j = 0; j < FJ; ++j)
           tm[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(db[j][e], da[i & 1][e], e == 0 ? v4f{} : tm[i & 1][j],
                                                                 0, 0, 0);
-        if (!kHead && i * FJ + e < LS) issue(i * FJ + e, LS);
+        if (!kHead) issue_at(i * FJ + e);
         if (i > 0) add(i > 0 ? i - 1 : 0, e, f[i > 0 ? i - 1 : 0]);
         else add(FI - 1, e, flast);
         if (e > 0) {
@@ -566,9 +603,20 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
 #pragma unroll
       for (int j = 0; j < FJ; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
+  // HALF: the first half of the step's stage has been read, its second has landed
+  auto middle = [&]() {
+    advance();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    land();
+    issue_scales();
+  };
   auto body = [&](auto self, auto ic) -> void {
     constexpr int i = decltype(ic)::value;
     if constexpr (i < FI - 1) {
+      if constexpr (C::HALF && i == kMid) {
+        pin();
+        middle();
+      }
       row(ic);
       self(self, std::integral_constant<int, i + 1>());
     }
@@ -590,7 +638,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     // A wave whose rows all lie past the tile's last one only loads its share.
     const bool active = t.row0 + wm * C::WTM < t.row_end;
     auto next = [&](int k) {     // ends step k: the next step's loads have landed
-      advance();
+      if constexpr (!C::HALF) advance();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage has been read
       land();
       stage = stage + 1 == ST ? 0 : stage + 1;
@@ -602,7 +650,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
 #pragma unroll
       for (int j = 0; j < FJ; ++j) tm[D - 1][j] = v4f{};
       for (int k = 0; k < nk; ++k) {
-        issue_scales();
+        if constexpr (!C::HALF) issue_scales();
         read_f(t, k);
         body(body, std::integral_constant<int, 0>());
         pin();
@@ -620,9 +668,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
       }
     } else {
       for (int k = 0; k < nk; ++k) {
-        issue_scales();
+        if constexpr (!C::HALF) issue_scales();
 #pragma unroll
-        for (int s = 0; s < LS; ++s) issue(s, LS);
+        for (int g = 0; g < GB; ++g) {
+          if (C::HALF && g == kMid * FJ) middle();
+          issue_at(g);
+        }
         next(k);
       }
     }
@@ -637,26 +688,31 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
     // row by row, 16 bytes a lane.
     if (active) {
       constexpr int ES = OUT == kOutBf16 || OUT == kOutF16 ? 2 : 4;
-      constexpr int RB = C::WTN * ES, CH = RB / 16;            // bytes and 16-byte chunks of a wave tile's row
-      constexpr int kFit = C::STAGE / C::WAVES / (16 * RB), kRows = kFit >= 4 && FI % 4 == 0 ? 4 : (kFit >= 2 ? 2 : 1);
+      // HALF: the late loads' part of the stage; a row of waves has its own
+      constexpr int kShare = C::HALF ? C::WTM / 2 * 128 / C::WN : C::STAGE / C::WAVES;
+      constexpr int kPairs = 16 * C::WTN * ES <= kShare ? FJ / 2 : 1;     // column pairs of fragments at a time
+      constexpr int RB = kPairs * 32 * ES, CH = RB / 16;       // bytes and 16-byte chunks of their rows
+      constexpr int kFit = kShare / (16 * RB), kRows = kFit >= 4 && FI % 4 == 0 ? 4 : (kFit >= 2 ? 2 : 1);
       static_assert(kFit >= 1 && FI % kRows == 0, "a fragment row fits a wave's share of a stage");
       int ln = lane;                       // opaque: nothing below is kept through the K loop
       asm volatile("" : "+v"(ln));
       const int x16 = ln & 15, q = ln >> 4;
-      uint8_t* mine = smem + lstep * C::STAGE + w * (C::STAGE / C::WAVES);
+      uint8_t* mine = smem + lstep * C::STAGE +
+                      (C::HALF ? wm * C::WTM * 128 + C::WTM / 2 * 128 + wn * kShare : w * kShare);
       auto slot = [](int row, int ch) { return row * RB + ((ch ^ (CH == 8 ? (row >> 1) & 7 : row & 15)) << 4); };
       const int64_t orow = (p.form == kGroupK ? (int64_t)t.g * p.rows : 0) + (int64_t)t.slice * p.rows;
       const int lrow = ln / CH, ch = ln % CH;                  // a store instruction: 64 / CH rows
       const int64_t row = t.row0 + wm * C::WTM + lrow, n = t.n0 + wn * C::WTN + ch * (16 / ES);
       uint8_t* dst = static_cast<uint8_t*>(p.out) + ((orow + row) * p.ldo + n) * ES;
-      const int64_t left = n < p.n ? t.row_end - row : 0;      // rows of the lane's column from here on
 #pragma unroll
-      for (int i0 = 0; i0 < FI; i0 += kRows) {
+      for (int b = 0; b < FI / kRows * (FJ / 2 / kPairs); ++b) {
+        const int i0 = b / (FJ / 2 / kPairs) * kRows, j0 = b % (FJ / 2 / kPairs) * kPairs;
+        const int64_t left = n + j0 * 32 < p.n ? t.row_end - row : 0;      // rows of the lane's column from here on
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
 #pragma unroll
-          for (int jp = 0; jp < FJ / 2; ++jp) {
-            const v4f lo4 = acc[i0 + i][2 * jp], hi4 = acc[i0 + i][2 * jp + 1];
+          for (int jp = 0; jp < kPairs; ++jp) {
+            const v4f lo4 = acc[i0 + i][2 * (j0 + jp)], hi4 = acc[i0 + i][2 * (j0 + jp) + 1];
             if constexpr (ES == 2) {
               constexpr bool F16 = OUT == kOutF16;
               *reinterpret_cast<uint4*>(mine + slot(16 * i + x16, 4 * jp + q)) =
@@ -673,7 +729,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
           const int r = 16 * i0 + c * (64 / CH);               // the instruction's first row in the wave tile
           v4f v = *reinterpret_cast<const v4f*>(mine + slot(c * (64 / CH) + lrow, ch));
           if (r < left) {
-            v4f* d = reinterpret_cast<v4f*>(dst + r * p.ldo * ES);
+            v4f* d = reinterpret_cast<v4f*>(dst + (r * p.ldo + j0 * 32) * ES);
             if constexpr (OUT == kOutF32Add) v = *d + v;
             if constexpr (POL != kPolKeep) __builtin_nontemporal_store(v, d);
             else *d = v;
