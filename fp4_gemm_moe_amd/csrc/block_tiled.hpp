@@ -201,8 +201,8 @@ __device__ __forceinline__ Tile make_tile(const BlockGemmArgs& p, const Table& t
     row0 = g * p.slot_rows + (int64_t)(mt - g * o.mt_per) * C::BM;
     row_end = (g + 1) * p.slot_rows;
     tl.slice = (int)ufirst((uint32_t)outer);
-    k0 = (int)((int64_t)p.nkb * outer / p.slices);
-    k1 = (int)((int64_t)p.nkb * (outer + 1) / p.slices);
+    k0 = p.nkb * outer / p.slices;               // nkb is below 2^16, slices at most 16
+    k1 = p.nkb * (outer + 1) / p.slices;
   } else if (p.form == kGroupK) {
     g = outer;
     row0 = (int64_t)mt * C::BM;
@@ -271,8 +271,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void block_gemm_tiled(BlockGemmArgs 
   if ((int)blockIdx.x >= per * nx) return;
   const int x = blockIdx.x % nx, ci = blockIdx.x / nx;
   const bool eighths = p.form == kUniform && p.groups == 1 && p.slices == 1;
-  const int first = eighths ? (int)((int64_t)ord.total * x / nx) + ci : 0;
-  const int last = eighths ? (int)((int64_t)ord.total * (x + 1) / nx) : ord.total;
+  auto eighth = [&](int i) { return nx == 8 ? (int)((int64_t)ord.total * i >> 3) : ord.total * i; };
+  const int first = eighths ? eighth(x) + ci : 0;
+  const int last = eighths ? eighth(x + 1) : ord.total;
   auto tile_at = [&](int round) -> int {
     if (eighths) return first + round * per;
     const int slot = x * per + ci, stride = per * nx;
