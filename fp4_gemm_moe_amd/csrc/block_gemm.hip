@@ -18,10 +18,13 @@ namespace {
 
 // ------------------------------------------------------------------ direct
 // Few rows: the weights are read once and bound the call.  A workgroup of W
-// waves takes 16 MF rows x 16 columns of one batch item; its waves take runs
-// of U K blocks in turn, each lane loading its operands from global memory
-// (U blocks in flight, the weights with the non-temporal policy), and their
-// sums meet in LDS.
+// waves takes 16 MF rows x 16 NF columns of one batch item; its waves take runs
+// of U K blocks in turn, each lane loading its operands from global memory (U
+// blocks in flight), and their sums meet in LDS in wave order.  No LDS staging:
+// a row's 128 codes are read once, in the lanes that multiply them.  Every wave
+// that fits keeps loads under way: W = 16, U = 2 was the best of W 4 .. 16, U 1 ..
+// 4 (1x17408x5120 17.6 us, 5.1 TB/s of weights, a large copy's rate; 16 rows of
+// A from the L2s take it to 26 us).  Non-temporal weight loads cost 1 to 17 %.
 template <int MF, int NF, int W, int U>
 __global__ __launch_bounds__(W * 64) void block_gemm_direct(BlockGemmArgs p) {
   __shared__ v4f part[W - 1][MF * NF][64];
@@ -55,11 +58,11 @@ __global__ __launch_bounds__(W * 64) void block_gemm_direct(BlockGemmArgs p) {
     for (int u = 0; u < U; ++u) {
       const int k0 = (kb + u) * 128;
 #pragma unroll
-      for (int j = 0; j < NF; ++j) bf[j][u] = load_pair<false>(bp[j] + k0, k0 < k16, k0 + 64 < k16);
+      for (int j = 0; j < NF; ++j) bf[j][u] = load_pair(bp[j] + k0, k0 < k16, k0 + 64 < k16);
       sv[u] = kb + u < p.nkb ? sb[kb + u] : 0.0f;
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        af[i][u] = load_pair<false>(ap[i] + k0, k0 < k16, k0 + 64 < k16);
+        af[i][u] = load_pair(ap[i] + k0, k0 < k16, k0 + 64 < k16);
         sav[i][u] = kb + u < p.nkb ? sap[i][kb + u] : 0.0f;
       }
     }
@@ -94,7 +97,9 @@ __global__ __launch_bounds__(W * 64) void block_gemm_direct(BlockGemmArgs p) {
 }
 
 // ------------------------------------------------------------------ K split
-// out = the slices' FP32 partial sums [slices, rows, n], added in slice order.
+// out = the slices' FP32 partial sums [slices, rows, n], added in slice order:
+// the same bits from run to run.  Its launch and the partials' way through the
+// caches bound it (77x5120x17408: 6 slices, 9.5 MB, 4.7 us of the call's 29).
 constexpr int kReduceThreads = 256;
 __global__ __launch_bounds__(kReduceThreads) void block_reduce(const float* __restrict__ partial, int slices,
                                                                int64_t rows, uint32_t nq, int64_t ldo, void* out,
@@ -115,8 +120,12 @@ __global__ __launch_bounds__(kReduceThreads) void block_reduce(const float* __re
 // FP32 results, go through FP16 operands with full FP32 sums.
 bool fast_path(const BlockGemmArgs& p) { return p.out_kind == kOutBf16 && p.nkb >= 4; }
 
-// A tile shape and what one of its steps takes on a full chip (microseconds,
-// measured at 2048 and 4096 x 17408 x 5120).
+// A tile shape and what one of its steps takes (microseconds), fitted to calls
+// of 17 to 4096 rows over 17408 x 5120 and 5120 x 17408.  A step costs less
+// where tiles share their weights on a full chip (256x256 2.10, 128x256 1.12,
+// 128x128 0.71, 64x128 0.48 at 4096 x 4096 x 4096) and where part of the chip
+// idles (256x256 1.47 at half of it); a model with both chose worse over 38
+// shapes (2048x17408x5120 189 -> 233 us, 128x17408x5120 36 -> 52 us).
 struct Shape {
   int tile, bm, bn;
   double us;
@@ -188,12 +197,15 @@ Plans plan_all(const BlockGemmArgs& p, const DeviceInfo& dev, bool fast, uint64_
 // Grouped forms, by the rows a group has (on average where only the device
 // knows them): few rows leave the weights' stream to bound the call, which the
 // deeper stages of the smaller tiles serve better; many share each weight tile.
+// Measured in us, K = 2048 and 4096, N = 4096: 32 slots of 64 rows 111 (64x128),
+// 122 (128x256), of 128 rows 169, 126, of 256 rows 174 (128x256), 138 (256x256);
+// contiguous groups of 256 rows on average 66.5 (128x256), 69 (256x256), of 512
+// rows 101, 95, of 1024 rows 175, 160.
 int plan_grouped(const BlockGemmArgs& p, bool fast) {
   const int64_t per = p.form == kContiguous ? up(p.rows, p.groups) : (p.form == kGroupK ? p.rows : p.slot_rows);
-  if (per <= 32) return kTile64x128;
+  if (per <= (p.form == kMasked ? 64 : 32)) return kTile64x128;
   if (!fast) return per <= 128 ? kTile128x128 : kTile256x128;
-  const int64_t limit = p.form == kContiguous ? 1024 : 128;
-  return per <= limit ? kTile128x256 : kTile256x256;
+  return per <= (p.form == kContiguous ? 384 : 128) ? kTile128x256 : kTile256x256;
 }
 
 bool direct_path(const BlockGemmArgs& p) { return p.form == kUniform && p.slot_rows <= 16; }

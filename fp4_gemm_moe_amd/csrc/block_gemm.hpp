@@ -34,13 +34,11 @@ __device__ __forceinline__ v4f dot16(v8i w, v8i x) {
   return acc;
 }
 
-// The 16 bytes at p and the 16 at p + 64; zeros where the flag is off.  NT:
-// with the non-temporal policy.
-template <bool NT>
+// The 16 bytes at p and the 16 at p + 64; zeros where the flag is off.
 __device__ __forceinline__ v8i load_pair(const uint8_t* p, bool in0, bool in1) {
   v4i u = {0, 0, 0, 0}, v = u;
-  if (in0) u = NT ? __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p)) : *reinterpret_cast<const v4i*>(p);
-  if (in1) v = NT ? __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p + 64)) : *reinterpret_cast<const v4i*>(p + 64);
+  if (in0) u = *reinterpret_cast<const v4i*>(p);
+  if (in1) v = *reinterpret_cast<const v4i*>(p + 64);
   return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 

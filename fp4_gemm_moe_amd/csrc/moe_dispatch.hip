@@ -25,8 +25,9 @@ namespace {
 // With more than one workgroup a first launch leaves every workgroup's counts
 // in the workspace, and each workgroup of the second adds up what lies ahead
 // of it.  The work is a few bytes a pair: launches and latency bound it, so a
-// run is as short as the workgroups can cover (one step a wave up to 1024
-// pairs: 512 pairs of 64 experts 13.6 us with runs of four steps, see below).
+// run is as short as the workgroups can cover: one step a wave up to 1024
+// pairs (512 pairs of 64 experts 4.4 us; with runs of four steps 13.6), 65536
+// pairs of 32 experts 4.7 + 5.9 us.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kHeld = 4;
 constexpr int kSortMaxBlocks = 256;
@@ -178,7 +179,8 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------ permute
 // A wave takes one 1 KB piece of one token's row, reads it once and writes it
-// to each of the token's rows (16 bytes a lane).  The last groups * kPadParts
+// to each of the token's rows (16 bytes a lane): the writes bound it, and the
+// reads are not repeated for each of them.  The last groups * kPadParts
 // workgroups write zeros to the padding rows.
 __global__ __launch_bounds__(kThreads) void permute_rows(const uint8_t* __restrict__ x, int64_t units, int64_t row_bytes,
                                                          int32_t pieces, const int32_t* __restrict__ row_map,
@@ -208,7 +210,9 @@ __global__ __launch_bounds__(kThreads) void permute_rows(const uint8_t* __restri
 }
 
 // The same with the row quantised to block-128 FP8 on the way: lane octets
-// take 128-blocks, 16 values a lane, as the row quantiser does.
+// take 128-blocks, 16 values a lane, as the row quantiser does.  Quantised once
+// a token, not once a pair.  16384 tokens top 4 of 4096 values: 75 us for 411 MB,
+// 5.5 TB/s, 83 with the sort (a copy's rate would make 80).
 template <bool F16>
 __global__ __launch_bounds__(kThreads) void permute_quant(const uint16_t* __restrict__ x, int64_t units, int64_t h,
                                                           int32_t nkb, int32_t pieces,
@@ -258,7 +262,8 @@ __global__ __launch_bounds__(kThreads) void permute_quant(const uint16_t* __rest
 // out[t] = sum over j of weights[t, j] y[row_map[t, j]] in FP32, in slot
 // order, rounded once.  A wave takes one 512-value piece of one token (16
 // bytes a lane and row); the rows of four slots are loaded before they are
-// added up.
+// added up.  The rows' bytes bound it: 1024 tokens top 8 of 2048 values 38 MB in
+// 8.6 us, 4.4 TB/s, launch included.
 template <bool F16>
 __global__ __launch_bounds__(kThreads) void combine_rows(const uint16_t* __restrict__ y, int64_t units, int64_t h,
                                                          int32_t pieces, const int32_t* __restrict__ row_map,
@@ -313,7 +318,8 @@ __global__ __launch_bounds__(kThreads) void combine_rows(const uint16_t* __restr
 // kilobyte, four loads in flight, then one reduction over the wave in a fixed
 // order.  dout's row comes from memory once and from a cache for the other
 // waves.  The bytes of y and dy bound it; with few tokens the chain of loads
-// behind a slot does, and a wave a slot keeps that chain one row long.
+// behind a slot does, and a wave a slot keeps that chain one row long.  16384
+// tokens top 4 of 4096 values: 1.21 GB in 204 to 224 us, 5.4 to 5.9 TB/s.
 template <bool F16, bool NT>
 __global__ __launch_bounds__(512) void combine_bwd(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ y,
                                                    int64_t tokens, int64_t h, const int32_t* __restrict__ row_map,

@@ -318,3 +318,46 @@ def test_many_tiles_of_one_step(dtype):
         else:
             hq.hq_block_gemm(H.dev(a), H.dev(sa), H.dev(b), H.dev(sb), out)
         H.check(out, ref, H.product_bound(ref, mag, k, dtype), f"{what} grouped={grouped}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_tiles_of_few_steps(dtype):
+    """More tiles than compute units, of none to nine K blocks each and with
+    partly filled rows and columns: a tile ends at every place of the stages and of
+    the scales' groups of four."""
+    what = f"short tiles {dtype}"
+    U.banner(what)
+    r = H.rng("few steps")
+    blocks = [2, 3, 1, 5, 0, 4, 9, 1, 1, 7, 6, 2, 8, 3, 0, 4, 5, 1]
+    E, m, n, K = len(blocks), 600, 1352, 128 * sum(blocks)
+    ends = 128 * np.cumsum(blocks)
+    (a, sa), (b, sb) = H.codes(r, m, K), H.codes(r, n, K, True)
+    out = torch.full((E, m, n), float("nan"), dtype=dtype, device="cuda")
+    hq.hq_block_group_k_gemm(H.dev(a), H.dev(sa), H.dev(b), H.dev(sb), U.dev_i32(ends, "cuda"), out)
+    for g in range(E):
+        lo, hi = int(ends[g]) - 128 * blocks[g], int(ends[g])
+        ref, mag = B.gemm(a[:, lo:hi], sa[:, lo // 128:hi // 128], b[:, lo:hi], sb[:, lo // 128:hi // 128])
+        # as above: a group of eight products loses less than 8 x 2^-13 of its largest
+        own = 2.0 ** -10 * mag if dtype is BF16 else 0.0
+        H.check(out[g], ref, H.product_bound(ref, mag, max(hi - lo, 128), dtype) + own, f"{what} group {g}")
+
+
+def test_split_of_large_tiles():
+    """Few large tiles over a long K: slices of it in a workspace, odd rows, and the
+    same bits from run to run."""
+    U.banner("K slices of 256 x 256 tiles")
+    r = H.rng("large slices")
+    m, n, k = 1000, 5120, 8192
+    (a, sa), (b, sb) = H.codes(r, m, k), H.codes(r, n, k, True)
+    da, dsa, db, dsb = H.dev(a), H.dev(sa), H.dev(b), H.dev(sb)
+    ws = torch.empty(hq.hq_block_gemm_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    outs = []
+    for _ in range(3):
+        out = torch.full((m, n), float("nan"), dtype=BF16, device="cuda")
+        hq.hq_block_gemm(da, dsa, db, dsb, out, workspace=ws)
+        outs.append(out)
+    rows = np.array([0, 1, 63, 64, 127, 128, 255, 256, 511, 700, 767, 768, 900, 999])
+    ref, mag = B.gemm(a[rows], sa[rows], b, sb)
+    H.check(outs[0][torch.from_numpy(rows).cuda()], ref, H.product_bound(ref, mag, k, BF16), "slices")
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
