@@ -23,6 +23,8 @@ Modules:
   quant    - MX (UE8M0 / 32) and NVFP4 (UE4M3 / 16 + FP32 global) quantisation
   gemm     - dense, batch, grouped-contiguous and grouped-masked scaled GEMMs
   swiglu   - SwiGLU followed by re-quantisation
+  dglu     - the backward grouped GEMM's dSwiGLU epilogue
+  block    - block-128 FP8 quantisation and products, the MoE token dispatch
 
 Every function is pinned by a ``-m "not gpu"`` test against something other
 than itself (exhaustive tables, brute force with exact rationals,
