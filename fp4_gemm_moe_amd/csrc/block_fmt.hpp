@@ -70,9 +70,11 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
 // N (a multiple of 4) values -> E4M3 codes of x / s, four to a dword.  For s
 // in [2^-56, 2^56] the quotients share one reciprocal: r = rcp(s) with a
 // Newton step, then t = x r and two FMA residual corrections
-// t += (x - s t) r, which give the correctly rounded quotient (P. Markstein,
+// t -= (s t - x) r, which give the correctly rounded quotient (P. Markstein,
 // "IA-64 and Elementary Functions", 2000) wherever it can round to anything
-// but a zero code; other scales take the IEEE division.
+// but a zero code; with the residual's sign this way round, a zero keeps x's
+// sign.  These quotients are at most 448 (1 + 2^-23), which rounds to 448, so
+// only other scales, which take the IEEE division, clamp theirs.
 template <int N>
 __device__ __forceinline__ void block_codes(const float (&x)[N], float s, uint32_t (&w)[N / 4]) {
   float q[N];
@@ -82,9 +84,8 @@ __device__ __forceinline__ void block_codes(const float (&x)[N], float s, uint32
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float t = x[i] * r;
-      t = __builtin_fmaf(__builtin_fmaf(-s, t, x[i]), r, t);
-      t = __builtin_fmaf(__builtin_fmaf(-s, t, x[i]), r, t);
-      q[i] = __builtin_copysignf(__builtin_amdgcn_fmed3f(t, -448.0f, 448.0f), x[i]);
+      t = __builtin_fmaf(__builtin_fmaf(s, t, -x[i]), -r, t);
+      q[i] = __builtin_fmaf(__builtin_fmaf(s, t, -x[i]), -r, t);
     }
   } else if (s <= 0x1p127f) {
 #pragma unroll
@@ -98,6 +99,30 @@ __device__ __forceinline__ void block_codes(const float (&x)[N], float s, uint32
     const int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
     w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], v, true);
   }
+}
+
+// Largest magnitudes of packed BF16 or FP16 pairs, as a packed pair: the
+// patterns without their signs, in integer order (NaN above Inf above the rest).
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                __builtin_bit_cast(u16x2, w & 0x7fff7fffu)));
+}
+
+// The FP32 pattern of the larger half of such a pair.
+template <bool F16>
+__device__ __forceinline__ uint32_t abs_max_bits(uint32_t m) {
+  const uint32_t h = (m & 0xffffu) > m >> 16 ? m & 0xffffu : m >> 16;
+  return __float_as_uint(half_lo<F16>(h));
+}
+
+// Largest |x| pattern of 16 packed values.
+template <bool F16>
+__device__ __forceinline__ uint32_t abs_max(const uint4& u, const uint4& v) {
+  uint32_t m = abs_max2(u.x & 0x7fff7fffu, u.y);
+  m = abs_max2(abs_max2(m, u.z), u.w);
+  m = abs_max2(abs_max2(m, v.x), v.y);
+  return abs_max_bits<F16>(abs_max2(abs_max2(m, v.z), v.w));
 }
 
 // Largest |x| pattern of N values.

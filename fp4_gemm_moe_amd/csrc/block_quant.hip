@@ -41,21 +41,23 @@ __global__ __launch_bounds__(kThreads) void block_rows_kernel(const uint16_t* __
   const int64_t c = (int64_t)kb * 128 + l * 16;
   const bool in = row < rows && c < k;
   float f[16];
+  uint32_t mx = 0;
   if (in) {
     const uint4* p = reinterpret_cast<const uint4*>(x + row * (SWIGLU ? 2 * k : k) + c);
-    unpack16<F16>(load_nt(p), load_nt(p + 1), f);
+    const uint4 v0 = load_nt(p), v1 = load_nt(p + 1);
+    unpack16<F16>(v0, v1, f);
     if constexpr (SWIGLU) {
       const uint4* pu = reinterpret_cast<const uint4*>(x + row * 2 * k + k + c);
       float u[16];
       unpack16<F16>(load_nt(pu), load_nt(pu + 1), u);
 #pragma unroll
       for (int i = 0; i < 16; ++i) f[i] = silu_mul(f[i], u[i]);
+      mx = abs_max(f);
+    } else {
+      mx = abs_max<F16>(v0, v1);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = 0.0f;
   }
-  const float s = block_scale(octet_max_u32(abs_max(f)));
+  const float s = block_scale(octet_max_u32(mx));
   if (!in) return;
   uint32_t w[4];
   block_codes(f, s, w);
@@ -67,6 +69,9 @@ __global__ __launch_bounds__(kThreads) void block_rows_kernel(const uint16_t* __
 // k0.. of one batch item).  Pass p of four gives lane octet (thread / 8) the
 // tile row 32 p + thread / 8, 16 values a lane.
 //   TRANS = false: one scale per tile (128 x 128 blocks), codes in x's layout.
+//   A lane's two loads share a cache line, which non-temporal ones did not keep
+//   between them (32 x [4096, 1536] 115.4 -> 109.5 us); the row form and the
+//   transposes measured 1 to 5 % slower with plain loads above 100 MB.
 //   TRANS = true: the codes go through LDS and leave as rows of q [k, m]; the
 //   scale is per tile (TWO_D) or per column of x (1 x 128 blocks of q's rows).
 template <bool F16, bool TWO_D, bool TRANS, bool NT>
@@ -96,15 +101,13 @@ __global__ __launch_bounds__(kThreads) void block_tile_kernel(const uint16_t* __
       v[p][0] = v[p][1] = make_uint4(0, 0, 0, 0);
       if (r < m && c < k) {
         const uint4* s = reinterpret_cast<const uint4*>(xb + r * k + c);
-        v[p][0] = load_nt(s);
-        v[p][1] = load_nt(s + 1);
+        v[p][0] = s[0];
+        v[p][1] = s[1];
       }
     }
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      float f[16];
-      unpack16<F16>(v[p][0], v[p][1], f);
-      const uint32_t a = abs_max(f);
+      const uint32_t a = abs_max<F16>(v[p][0], v[p][1]);
       mx = a > mx ? a : mx;
     }
     mx = wave_max_u32(mx);
@@ -136,14 +139,10 @@ __global__ __launch_bounds__(kThreads) void block_tile_kernel(const uint16_t* __
       const int64_t r = m0 + 32 * w + i;
       v[i] = r < m && c < k ? __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(xb + r * k + c)) : 0u;
     }
-    uint32_t mlo = 0, mhi = 0;
+    uint32_t m2 = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t a = __float_as_uint(half_lo<F16>(v[i])) & 0x7fffffffu;
-      const uint32_t b = __float_as_uint(half_hi<F16>(v[i])) & 0x7fffffffu;
-      mlo = a > mlo ? a : mlo;
-      mhi = b > mhi ? b : mhi;
-    }
+    for (int i = 0; i < 32; ++i) m2 = abs_max2(m2, v[i]);
+    uint32_t mlo = __float_as_uint(half_lo<F16>(m2)), mhi = __float_as_uint(half_hi<F16>(m2));
     float slo, shi;
     if constexpr (TWO_D) {
       uint32_t mx = wave_max_u32(mlo > mhi ? mlo : mhi);

@@ -236,15 +236,15 @@ __global__ __launch_bounds__(kThreads) void permute_quant(const uint16_t* __rest
   const int64_t t = u / pieces;
   const int64_t c = (u - t * pieces) * 1024 + lane * 16;
   float f[16];
+  uint32_t mx = 0;
   const bool in = c < h;
   if (in) {
     const uint4* p = reinterpret_cast<const uint4*>(x + t * h + c);
-    unpack16<F16>(load_nt(p), load_nt(p + 1), f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+    const uint4 v0 = load_nt(p), v1 = load_nt(p + 1);
+    unpack16<F16>(v0, v1, f);
+    mx = abs_max<F16>(v0, v1);
   }
-  const float s = block_scale(octet_max_u32(abs_max(f)));
+  const float s = block_scale(octet_max_u32(mx));
   if (!in) return;
   uint32_t o[4];
   block_codes(f, s, o);
