@@ -611,11 +611,18 @@ def hq_fused_swiglu_block_quant(x, q, sf, group_end=None):
         _in_flag(x)))
 
 
-def hq_block_gemm_workspace_size(m, n, k, batch=1):
+def hq_block_gemm_workspace_size(m, n, k, batch=1, out_dtype=None):
     """Bytes of workspace a dense or batched block product of this shape uses
-    on the current device (0: it never splits K)."""
+    on the current device (0: it never splits K) for results of out_dtype
+    (bfloat16, float16, float32, accumulated or not).  None: the bytes that are
+    enough for any of them."""
+    if out_dtype is None:
+        return max(hq_block_gemm_workspace_size(m, n, k, batch, t) for t in (torch.bfloat16, torch.float32))
+    flags = _OUT_FLAGS.get(out_dtype)
+    if flags is None:
+        raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
     out = ctypes.c_uint64(0)
-    _check(load().hq_block_gemm_workspace_size(0, batch, m, n, k, ctypes.byref(out)))
+    _check(load().hq_block_gemm_workspace_size(flags, batch, m, n, k, ctypes.byref(out)))
     return int(out.value)
 
 
@@ -624,7 +631,7 @@ def hq_block_gemm(a, sfa, b, sfb, out, accumulate=False, workspace=None):
     (2-D, or 3-D with a batch): a uint8, sfa float32 [.., m, ceil(k/128)], b
     uint8, sfb float32 [.., ceil(n/128), ceil(k/128)].  out is bfloat16, float16
     or float32 (accumulate: out += the product).  With a workspace (any dtype,
-    hq_block_gemm_workspace_size bytes) the call may split K."""
+    hq_block_gemm_workspace_size bytes for this out) the call may split K."""
     m, k = a.shape[-2:]
     n = b.shape[-2]
     batch = a.shape[0] if a.dim() == 3 else 1

@@ -520,8 +520,9 @@ hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t r
  *
  * hq_block_gemm: dense (batch 1) or batched; a [batch, m, k], b [batch, n, k],
  * out [batch, m, n].  hq_block_gemm_workspace_size gives the bytes of FP32
- * workspace that this shape uses when it splits K (0: never); with a smaller
- * or no workspace the call runs unsplit.  No call uses more than
+ * workspace that this shape uses when it splits K (0: never), for the flags of
+ * the call: the result's type decides how K is split.  With a smaller or no
+ * workspace the call runs unsplit.  No call uses more than
  * HQ_BLOCK_WORKSPACE_BYTES.  Two calls in flight need two workspaces.
  */
 #define HQ_BLOCK_WORKSPACE_BYTES (64u << 20)
