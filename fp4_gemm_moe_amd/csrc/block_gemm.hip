@@ -128,8 +128,10 @@ __global__ __launch_bounds__(kReduceThreads) void block_reduce(const float* __re
 // BF16 results of four K blocks or more take the FP8 matrix instructions: their
 // sums are off by 1.5e-5 of the norm at K = 128 and less with every further
 // block, a hundredth of the BF16 rounding at four.  Shorter sums, and FP16 and
-// FP32 results, go through FP16 operands with full FP32 sums.
-bool fast_path(const BlockGemmArgs& p) { return p.out_kind == kOutBf16 && p.nkb >= 4; }
+// FP32 results, go through FP16 operands with full FP32 sums.  So do sums over
+// the groups' ranges of K: only the device knows their lengths, and one of a
+// single block has no further ones to average over.
+bool fast_path(const BlockGemmArgs& p) { return p.out_kind == kOutBf16 && p.nkb >= 4 && p.form != kGroupK; }
 
 // A tile shape and what one of its steps takes (microseconds), fitted to calls
 // of 17 to 4096 rows over 17408 x 5120 and 5120 x 17408.  A step costs less

@@ -502,13 +502,12 @@ hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t r
  * to BF16 (FP16 with HQ_OUT_FP16; kept in FP32 with HQ_OUT_FP32; added in
  * FP32 to out with HQ_OUT_FP32 | HQ_ACCUMULATE).  A product of two scales
  * has to be a finite FP32 number.
- * Precision of the inner sums: FP16 and FP32 results, and any result of k <
- * 512, multiply the codes exactly and add in FP32.  BF16 results of a longer k
- * use the FP8 matrix instructions, which align eight neighbouring products to
- * the largest of them and keep 13 bits below it: an inner sum is off by less
- * than 2^-10 of its sum of magnitudes, and by about 1.5e-5 of the product of
- * the operands' norms for random codes (for hq_block_group_k_gemm k is
- * k_total, whatever the ranges' lengths).
+ * Precision of the inner sums: FP16 and FP32 results, any result of k < 512 and
+ * all of hq_block_group_k_gemm multiply the codes exactly and add in FP32.
+ * Other BF16 results use the FP8 matrix instructions, which align eight
+ * neighbouring products to the largest of them and keep 13 bits below it: an
+ * inner sum is off by less than 2^-10 of its sum of magnitudes, and by about
+ * 1.5e-5 of the product of the operands' norms for random codes.
  *   a [.., k] codes, sfa [.., ceil(k/128)] (1 x 128 blocks);
  *   b [.., n, k] codes, sfb [.., ceil(n/128), ceil(k/128)] (128 x 128 blocks).
  * k % 32 == 0, n % 8 == 0, 256 k < 2^31; a, b, out and the workspace 16-byte
