@@ -11,6 +11,7 @@ loudly (build it with ``python -m fp4_gemm_moe_amd.build``).
 PyTorch is used for device memory and streams only.
 """
 import ctypes
+import math
 import os
 
 import torch
@@ -736,7 +737,7 @@ def hq_moe_permute(x, row_map, group_end, counts, out):
     rows = out.shape[0]
     if x.shape[0] != T or x.shape[1:] != out.shape[1:]:
         raise ValueError("x and row_map must have the same tokens, x and out the same rows")
-    width = out[:1].numel() * out.element_size() if rows > 0 else x[:1].numel() * x.element_size()
+    width = math.prod(x.shape[1:]) * x.element_size()
     ge, cn, E = _pads(group_end, counts)
     _check(load().hq_moe_permute(
         _raw_stream(x), _arg(x, "x", x.dtype, x.numel()), T, width, _arg(row_map, "row_map", torch.int32, T * topk),
