@@ -123,10 +123,11 @@ hq_status check_width(const char* what, int64_t h, int64_t step) {
   return HQ_OK;
 }
 
-// Workgroups of a launch stay below 2^31: `per_row` pieces of every row.
-hq_status check_grid(const char* what, int64_t rows, int64_t per_row) {
-  if (rows > 0 && per_row > (int64_t)kI32 * 2 / rows)
-    return fail(HQ_ERR_SHAPE, "%s: problem too large for one launch", what);
+// A launch's work items stay below the limit of one dimension.
+hq_status check_grid(const char* what, int64_t workgroups, int threads) {
+  if (workgroups > (hq::kMaxWorkItems - 1) / threads)
+    return fail(HQ_ERR_SHAPE, "%s: problem too large: %lld workgroups of %d threads pass 2^32 work items", what,
+                (long long)workgroups, threads);
   return HQ_OK;
 }
 
@@ -145,7 +146,10 @@ hq_status hq_block_quant(void* stream, const uint16_t* x, int64_t batch, int64_t
     return fail(HQ_ERR_SHAPE, "%s: k=%lld must be a positive multiple of 32 below 2^31", what, (long long)k);
   if ((flags & HQ_TRANSPOSE) && m % 32 != 0)
     return fail(HQ_ERR_SHAPE, "%s: m=%lld must be a multiple of 32 with HQ_TRANSPOSE", what, (long long)m);
-  if ((st = check_grid(what, batch * m, (k + 127) / 128)) != HQ_OK) return st;
+  const bool tiles = (flags & (HQ_BLOCK_2D | HQ_TRANSPOSE)) != 0;
+  if ((st = check_grid(what, tiles ? hq::quant_tile_groups(batch, m, k) : hq::quant_row_groups(batch * m, k),
+                       hq::kQuantThreads)) != HQ_OK)
+    return st;
   if (batch == 0 || m == 0) return ok();
   if (!x || !q || !sf) return fail(HQ_ERR_NULL, "%s: x, q and sf are required", what);
   if (!aligned16(x) || !aligned16(q)) return fail(HQ_ERR_ALIGN, "%s: x and q must be 16-byte aligned", what);
@@ -166,7 +170,7 @@ hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t r
   if (group_end != nullptr && (st = check_groups(what, num_groups)) != HQ_OK) return st;
   if (rows < 0 || rows > kI32) return fail(HQ_ERR_SHAPE, "%s: rows=%lld out of range", what, (long long)rows);
   if ((st = check_width(what, h, 32)) != HQ_OK) return st;
-  if ((st = check_grid(what, rows, (h + 127) / 128)) != HQ_OK) return st;
+  if ((st = check_grid(what, hq::quant_row_groups(rows, h), hq::kQuantThreads)) != HQ_OK) return st;
   if (rows == 0) return ok();
   if (!x || !q || !sf) return fail(HQ_ERR_NULL, "%s: x, q and sf are required", what);
   if (!aligned16(x) || !aligned16(q)) return fail(HQ_ERR_ALIGN, "%s: x and q must be 16-byte aligned", what);
@@ -339,14 +343,17 @@ hq_status hq_moe_permute(void* stream, const uint8_t* x, int64_t num_tokens, int
   if (row_bytes <= 0 || row_bytes % 16 != 0 || row_bytes > kI32)
     return fail(HQ_ERR_SHAPE, "%s: row_bytes=%lld must be a positive multiple of 16 below 2^31", what,
                 (long long)row_bytes);
-  if ((st = check_grid(what, num_tokens, (row_bytes + 1023) / 1024)) != HQ_OK) return st;
+  const hq::PadRows pad{group_end, counts, num_groups};
+  if ((st = check_grid(what, hq::piece_groups(num_tokens, row_bytes, 1024) + hq::pad_groups(pad), hq::kMoeThreads)) !=
+      HQ_OK)
+    return st;
   if (max_rows == 0) return ok();
   if (!out || (num_tokens > 0 && (!x || !row_map))) return fail(HQ_ERR_NULL, "%s: x, row_map and out are required", what);
   if (!aligned16(x) || !aligned16(out)) return fail(HQ_ERR_ALIGN, "%s: x and out must be 16-byte aligned", what);
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
-  return launched(hq::launch_moe_permute((hipStream_t)stream, x, num_tokens, row_bytes, row_map, topk,
-                                         hq::PadRows{group_end, counts, num_groups}, max_rows, out),
+  return launched(hq::launch_moe_permute((hipStream_t)stream, x, num_tokens, row_bytes, row_map, topk, pad, max_rows,
+                                         out),
                   what);
 }
 
@@ -360,7 +367,10 @@ hq_status hq_moe_permute_block_quant(void* stream, const uint16_t* x, int64_t nu
   if (st != HQ_OK) return st;
   if ((st = check_pad(what, group_end, counts, num_groups)) != HQ_OK) return st;
   if ((st = check_width(what, hidden, 32)) != HQ_OK) return st;
-  if ((st = check_grid(what, num_tokens, (hidden + 1023) / 1024)) != HQ_OK) return st;
+  const hq::PadRows pad{group_end, counts, num_groups};
+  if ((st = check_grid(what, hq::piece_groups(num_tokens, hidden, 1024) + hq::pad_groups(pad), hq::kMoeThreads)) !=
+      HQ_OK)
+    return st;
   if (max_rows == 0) return ok();
   if (!q || !sf || (num_tokens > 0 && (!x || !row_map)))
     return fail(HQ_ERR_NULL, "%s: x, row_map, q and sf are required", what);
@@ -368,9 +378,8 @@ hq_status hq_moe_permute_block_quant(void* stream, const uint16_t* x, int64_t nu
   if (!aligned4(sf)) return fail(HQ_ERR_ALIGN, "%s: sf must be 4-byte aligned", what);
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
-  return launched(hq::launch_moe_permute_block_quant((hipStream_t)stream, x, num_tokens, hidden, row_map, topk,
-                                                     hq::PadRows{group_end, counts, num_groups}, max_rows, q, sf,
-                                                     (flags & HQ_IN_FP16) != 0),
+  return launched(hq::launch_moe_permute_block_quant((hipStream_t)stream, x, num_tokens, hidden, row_map, topk, pad,
+                                                     max_rows, q, sf, (flags & HQ_IN_FP16) != 0),
                   what);
 }
 
@@ -381,7 +390,7 @@ hq_status hq_moe_combine(void* stream, const uint16_t* y, int64_t num_tokens, in
   hq_status st = check_map(what, Map{num_tokens, topk, max_rows});
   if (st != HQ_OK) return st;
   if ((st = check_width(what, hidden, 8)) != HQ_OK) return st;
-  if ((st = check_grid(what, num_tokens, (hidden + 511) / 512)) != HQ_OK) return st;
+  if ((st = check_grid(what, hq::piece_groups(num_tokens, hidden, 512), hq::kMoeThreads)) != HQ_OK) return st;
   if (num_tokens == 0) return ok();
   if (!out || !row_map || (max_rows > 0 && !y)) return fail(HQ_ERR_NULL, "%s: y, row_map and out are required", what);
   if (!aligned16(y) || !aligned16(out)) return fail(HQ_ERR_ALIGN, "%s: y and out must be 16-byte aligned", what);
@@ -403,6 +412,8 @@ hq_status hq_moe_combine_backward(void* stream, const uint16_t* dout, const uint
   if (st != HQ_OK) return st;
   if ((st = check_pad(what, group_end, counts, num_groups)) != HQ_OK) return st;
   if ((st = check_width(what, hidden, 8)) != HQ_OK) return st;
+  const hq::PadRows pad{group_end, counts, num_groups};
+  if ((st = check_grid(what, num_tokens + hq::pad_groups(pad), 64 * hq::combine_bwd_waves(topk))) != HQ_OK) return st;
   if (num_tokens == 0 && (max_rows == 0 || group_end == nullptr)) return ok();
   if ((max_rows > 0 && (!dy || !y)) || (num_tokens > 0 && (!dout || !row_map || !weights || !dweights)))
     return fail(HQ_ERR_NULL, "%s: dout, y, row_map, weights, dy and dweights are required", what);
@@ -413,8 +424,7 @@ hq_status hq_moe_combine_backward(void* stream, const uint16_t* dout, const uint
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_moe_combine_backward((hipStream_t)stream, dout, y, num_tokens, hidden, row_map, topk,
-                                                  weights, hq::PadRows{group_end, counts, num_groups}, max_rows, dy,
-                                                  dweights, (flags & HQ_IN_FP16) != 0),
+                                                  weights, pad, max_rows, dy, dweights, (flags & HQ_IN_FP16) != 0),
                   what);
 }
 

@@ -221,7 +221,10 @@ int plan_grouped(const BlockGemmArgs& p, bool fast) {
   return per <= (p.form == kContiguous ? 384 : 128) ? kTile128x256 : kTile256x256;
 }
 
-bool direct_path(const BlockGemmArgs& p) { return p.form == kUniform && p.slot_rows <= 16; }
+// At most 16 rows, and columns that fit one launch (1024 threads for 16 of them).
+bool direct_path(const BlockGemmArgs& p) {
+  return p.form == kUniform && p.slot_rows <= 16 && up(p.n, 16) <= (kMaxWorkItems - 1) / 1024;
+}
 
 hipError_t launch_tiled(hipStream_t s, BlockGemmArgs p, const DeviceInfo& dev, bool fast, const Plan& pl, void* ws) {
   const BlockGemmArgs whole = p;

@@ -39,6 +39,19 @@ struct BlockGemmArgs {
   int32_t slices;            // kUniform: K slices; out then holds [slices, rows, n] FP32 partial sums
 };
 
+// A launch holds fewer than 2^32 work items along a dimension of its grid.  The
+// functions below say how many workgroups a call takes; the C-ABI layer refuses
+// calls that do not fit, so the kernels' workgroup numbers are below 2^24 (256
+// threads a workgroup) and 128-blocks of a row form below 2^29.
+constexpr int64_t kMaxWorkItems = (int64_t)1 << 32;
+
+// 256 threads: 32 blocks of 1 x 128, or one 128 x 128 tile.
+constexpr int kQuantThreads = 256;
+inline int64_t quant_row_groups(int64_t rows, int64_t k) { return (rows * ((k + 127) / 128) + 31) / 32; }
+inline int64_t quant_tile_groups(int64_t batch, int64_t m, int64_t k) {
+  return batch * ((m + 127) / 128) * ((k + 127) / 128);
+}
+
 hipError_t launch_block_gemm(hipStream_t s, const BlockGemmArgs& args, const DeviceInfo& dev, void* workspace,
                              uint64_t workspace_bytes);
 // Bytes of workspace that a dense or batch call of this shape uses.
@@ -60,6 +73,18 @@ struct PadRows {
   const int32_t* counts;
   int32_t groups;
 };
+// Four units of 64 lanes a workgroup of 256 threads: pieces of `piece` bytes or
+// values of every token's row; then kPadParts workgroups for each group's
+// padding rows.
+constexpr int kMoeThreads = 256;
+constexpr int kPadParts = 8;
+inline int64_t pad_groups(const PadRows& pad) { return pad.group_end != nullptr ? (int64_t)pad.groups * kPadParts : 0; }
+inline int64_t piece_groups(int64_t tokens, int64_t width, int64_t piece) {
+  return (tokens * ((width + piece - 1) / piece) + 3) / 4;
+}
+// The combination's gradient: a workgroup a token, a wave for each of its slots
+// (four waves at least, for the padding rows, and eight at most).
+inline int combine_bwd_waves(int topk) { return topk > 8 ? 8 : (topk < 4 ? 4 : topk); }
 hipError_t launch_moe_permute(hipStream_t s, const uint8_t* x, int64_t tokens, int64_t row_bytes,
                               const int32_t* row_map, int32_t topk, PadRows pad, int64_t max_rows, uint8_t* out);
 hipError_t launch_moe_permute_block_quant(hipStream_t s, const uint16_t* x, int64_t tokens, int64_t h,

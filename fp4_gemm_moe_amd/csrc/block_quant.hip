@@ -12,7 +12,7 @@
 namespace hq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kQuantThreads;
 
 // Row form, and SwiGLU (x [rows, 2k] = [gate | up], y = up * silu(gate)).
 // Eight lanes take a 128-block, 16 values each: two 16-byte loads, one 16-byte
@@ -23,17 +23,10 @@ template <bool F16, bool SWIGLU, bool NT>
 __global__ __launch_bounds__(kThreads) void block_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t k,
                                                               int32_t nkb, const int32_t* __restrict__ last_end,
                                                               uint8_t* __restrict__ q, float* __restrict__ sf) {
-  const int64_t o = (int64_t)blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);
+  const uint32_t o = blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);      // below 2^29
   const int l = threadIdx.x & 7;
-  int64_t row;
-  int kb;
-  if (rows * nkb < 0xFFFFFF00ll) {
-    row = (uint32_t)o / (uint32_t)nkb;
-    kb = (int)((uint32_t)o - (uint32_t)row * (uint32_t)nkb);
-  } else {
-    row = o / nkb;
-    kb = (int)(o - row * nkb);
-  }
+  const int64_t row = o / (uint32_t)nkb;
+  const int kb = (int)(o - (uint32_t)row * (uint32_t)nkb);
   if (last_end != nullptr) {
     const int64_t e = *last_end;
     rows = e < 0 ? 0 : (e < rows ? e : rows);
@@ -200,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void block_tile_kernel(const uint16_t* __
 template <bool SWIGLU>
 hipError_t launch_rows(hipStream_t s, const uint16_t* x, int64_t rows, int64_t k, const int32_t* last_end, uint8_t* q,
                        float* sf, bool fp16) {
-  const int64_t nkb = (k + 127) / 128, blocks = (rows * nkb + kThreads / 8 - 1) / (kThreads / 8);
+  const int64_t nkb = (k + 127) / 128, blocks = quant_row_groups(rows, k);
   const bool nt = rows * k > kStreamBytes;
 #define HQ_ROWS(F, N)                                                                                                \
   hipLaunchKernelGGL((block_rows_kernel<F, SWIGLU, N>), dim3((unsigned)blocks), dim3(kThreads), 0, s, x, rows, k,   \
@@ -219,8 +212,8 @@ hipError_t launch_tiles(hipStream_t s, const uint16_t* x, int64_t batch, int64_t
   const int64_t tk = (k + 127) / 128, tm = (m + 127) / 128;
   const bool nt = batch * m * k > kStreamBytes;
 #define HQ_TILE(F, N)                                                                                          \
-  hipLaunchKernelGGL((block_tile_kernel<F, TWO_D, TRANS, N>), dim3((unsigned)(batch * tm * tk)), dim3(kThreads), 0, \
-                     s, x, m, k, (int32_t)tm, (int32_t)tk, q, sf)
+  hipLaunchKernelGGL((block_tile_kernel<F, TWO_D, TRANS, N>), dim3((unsigned)quant_tile_groups(batch, m, k)),          \
+                     dim3(kThreads), 0, s, x, m, k, (int32_t)tm, (int32_t)tk, q, sf)
   if (fp16 && nt) HQ_TILE(true, true);
   else if (fp16) HQ_TILE(true, false);
   else if (nt) HQ_TILE(false, true);

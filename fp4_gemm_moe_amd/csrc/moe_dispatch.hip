@@ -174,8 +174,7 @@ __device__ __forceinline__ void pad_range(const PadRows& p, int g, int64_t max_r
   r1 = e < max_rows ? e : max_rows;
 }
 
-constexpr int kPadParts = 8;    // workgroups that share a group's padding rows
-constexpr int kThreads = 256;
+constexpr int kThreads = kMoeThreads;
 
 // ------------------------------------------------------------------ permute
 // A wave takes one 1 KB piece of one token's row, reads it once and writes it
@@ -404,13 +403,12 @@ hipError_t launch_moe_sort(hipStream_t s, const int64_t* ids, int64_t pairs, int
   return hipGetLastError();
 }
 
-static int64_t pad_blocks(const PadRows& pad) { return pad.group_end != nullptr ? (int64_t)pad.groups * kPadParts : 0; }
-
 hipError_t launch_moe_permute(hipStream_t s, const uint8_t* x, int64_t tokens, int64_t row_bytes,
                               const int32_t* row_map, int32_t topk, PadRows pad, int64_t max_rows, uint8_t* out) {
-  const int64_t pieces = (row_bytes + 1023) / 1024, units = tokens * pieces, blocks = (units + 3) / 4;
-  if (blocks + pad_blocks(pad) == 0) return hipSuccess;
-  hipLaunchKernelGGL(permute_rows, dim3((unsigned)(blocks + pad_blocks(pad))), dim3(kThreads), 0, s, x, units,
+  const int64_t pieces = (row_bytes + 1023) / 1024, units = tokens * pieces;
+  const int64_t blocks = piece_groups(tokens, row_bytes, 1024);
+  if (blocks + pad_groups(pad) == 0) return hipSuccess;
+  hipLaunchKernelGGL(permute_rows, dim3((unsigned)(blocks + pad_groups(pad))), dim3(kThreads), 0, s, x, units,
                      row_bytes, (int32_t)pieces, row_map, topk, pad, max_rows, blocks, out);
   return hipGetLastError();
 }
@@ -418,9 +416,9 @@ hipError_t launch_moe_permute(hipStream_t s, const uint8_t* x, int64_t tokens, i
 hipError_t launch_moe_permute_block_quant(hipStream_t s, const uint16_t* x, int64_t tokens, int64_t h,
                                           const int32_t* row_map, int32_t topk, PadRows pad, int64_t max_rows,
                                           uint8_t* q, float* sf, bool fp16) {
-  const int64_t pieces = (h + 1023) / 1024, units = tokens * pieces, blocks = (units + 3) / 4;
-  if (blocks + pad_blocks(pad) == 0) return hipSuccess;
-  const dim3 grid((unsigned)(blocks + pad_blocks(pad)));
+  const int64_t pieces = (h + 1023) / 1024, units = tokens * pieces, blocks = piece_groups(tokens, h, 1024);
+  if (blocks + pad_groups(pad) == 0) return hipSuccess;
+  const dim3 grid((unsigned)(blocks + pad_groups(pad)));
   const int32_t nkb = (int32_t)((h + 127) / 128);
   if (fp16)
     hipLaunchKernelGGL(permute_quant<true>, grid, dim3(kThreads), 0, s, x, units, h, nkb, (int32_t)pieces, row_map, topk,
@@ -434,7 +432,7 @@ hipError_t launch_moe_permute_block_quant(hipStream_t s, const uint16_t* x, int6
 hipError_t launch_moe_combine(hipStream_t s, const uint16_t* y, int64_t tokens, int64_t h, const int32_t* row_map,
                               int32_t topk, const float* weights, int64_t max_rows, uint16_t* out, bool fp16) {
   const int64_t pieces = (h + 511) / 512, units = tokens * pieces;
-  const dim3 grid((unsigned)((units + 3) / 4));
+  const dim3 grid((unsigned)piece_groups(tokens, h, 512));
   if (fp16)
     hipLaunchKernelGGL(combine_rows<true>, grid, dim3(kThreads), 0, s, y, units, h, (int32_t)pieces, row_map, topk,
                        weights, max_rows, out);
@@ -447,9 +445,9 @@ hipError_t launch_moe_combine(hipStream_t s, const uint16_t* y, int64_t tokens, 
 hipError_t launch_moe_combine_backward(hipStream_t s, const uint16_t* dout, const uint16_t* y, int64_t tokens,
                                        int64_t h, const int32_t* row_map, int32_t topk, const float* weights,
                                        PadRows pad, int64_t max_rows, uint16_t* dy, float* dweights, bool fp16) {
-  const int64_t blocks = tokens + pad_blocks(pad);
+  const int64_t blocks = tokens + pad_groups(pad);
   if (blocks == 0) return hipSuccess;
-  const int waves = topk > 8 ? 8 : (topk < 4 ? 4 : topk);      // four at least, for the padding rows
+  const int waves = combine_bwd_waves(topk);
   const bool nt = max_rows * h * 2 > kStreamBytes;
 #define HQ_BWD(F, N)                                                                                               \
   hipLaunchKernelGGL((combine_bwd<F, N>), dim3((unsigned)blocks), dim3(64 * waves), 0, s, dout, y, tokens, h, row_map, \

@@ -478,6 +478,8 @@ hq_status hq_prefill_permute_to_masked_gemm(void* stream, const uint8_t* x, int6
  * activations.  With HQ_BLOCK_2D the blocks are 128 x 128: sf
  * [batch, ceil(rows/128), ceil(cols/128)] of q's rows and columns.
  *   k % 32 == 0; 0 <= batch <= 65535; x, q 16-byte aligned, sf 4-byte aligned.
+ * One launch takes fewer than 2^29 blocks of 1 x 128, or 2^24 of 128 x 128 (and
+ * tiles of that size with HQ_TRANSPOSE): HQ_ERR_SHAPE from there on.
  */
 hq_status hq_block_quant(void* stream, const uint16_t* x, int64_t batch, int64_t m,
                          int64_t k, uint8_t* q, float* sf, uint32_t flags);
@@ -487,7 +489,7 @@ hq_status hq_block_quant(void* stream, const uint16_t* x, int64_t batch, int64_t
  * (BF16, FP16 with HQ_IN_FP16), y = up * gate / (1 + exp(-gate)) in FP32, then
  * q [rows, h], sf [rows, ceil(h/128)] as hq_block_quant in 1 x 128 blocks.
  * group_end (optional, device int32 [num_groups]): rows at or past its last
- * value are neither read nor written.  h % 32 == 0.
+ * value are neither read nor written.  h % 32 == 0; fewer than 2^29 blocks.
  */
 hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t rows,
                                       int64_t h, const int32_t* group_end,
@@ -594,7 +596,9 @@ hq_status hq_moe_sort_workspace_size(int64_t num_tokens, int32_t topk,
  * and counts (both or neither) the padding rows, those of a group past its
  * count, are written as zeros (scales 2^-126), as a product over K ranges
  * needs them; other rows are not written.  Values are BF16 (FP16 with
- * HQ_IN_FP16, for every 16-bit tensor of the call).
+ * HQ_IN_FP16, for every 16-bit tensor of the call).  One launch takes about 2^26
+ * pieces of the tokens' rows (1 KB of bytes or 1024 values to permute, 512 values
+ * to combine), or 2^23 to 2^24 tokens in the gradient: HQ_ERR_SHAPE beyond.
  *
  * hq_moe_permute: out[row_map[t, j]] = x[t], rows of row_bytes bytes (a
  * multiple of 16), copied bit for bit.  Its gradient is hq_moe_combine with
