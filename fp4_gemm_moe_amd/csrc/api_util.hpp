@@ -23,6 +23,7 @@ __attribute__((visibility("hidden"))) hq_status current_device(DeviceInfo* out);
 __attribute__((visibility("hidden"))) hq_status launched(hipError_t e, const char* what);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace api

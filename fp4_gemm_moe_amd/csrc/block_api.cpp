@@ -9,6 +9,7 @@
 
 using hq::api::aligned16;
 using hq::api::aligned4;
+using hq::api::aligned8;
 using hq::api::current_device;
 using hq::api::fail;
 using hq::api::kI32;
@@ -115,6 +116,13 @@ hq_status check_pad(const char* what, const int32_t* group_end, const int32_t* c
   return HQ_OK;
 }
 
+// The int32 tensors of those calls; any of them may be null.
+hq_status check_index(const char* what, const int32_t* row_map, const int32_t* group_end, const int32_t* counts) {
+  if (!aligned4(row_map) || !aligned4(group_end) || !aligned4(counts))
+    return fail(HQ_ERR_ALIGN, "%s: row_map, group_end and counts must be 4-byte aligned", what);
+  return HQ_OK;
+}
+
 // A width of h halves: 16-byte rows.
 hq_status check_width(const char* what, int64_t h, int64_t step) {
   if (h <= 0 || h % step != 0 || h > kI32 / 16)
@@ -174,7 +182,8 @@ hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t r
   if (rows == 0) return ok();
   if (!x || !q || !sf) return fail(HQ_ERR_NULL, "%s: x, q and sf are required", what);
   if (!aligned16(x) || !aligned16(q)) return fail(HQ_ERR_ALIGN, "%s: x and q must be 16-byte aligned", what);
-  if (!aligned4(sf)) return fail(HQ_ERR_ALIGN, "%s: sf must be 4-byte aligned", what);
+  if (!aligned4(sf) || !aligned4(group_end))
+    return fail(HQ_ERR_ALIGN, "%s: sf and group_end must be 4-byte aligned", what);
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_swiglu_block_quant((hipStream_t)stream, x, rows, h,
@@ -234,6 +243,7 @@ hq_status hq_block_group_contiguous_gemm(void* stream, uint32_t flags, const uin
   if ((st = check_product(what, flags, p, &noop)) != HQ_OK) return st;
   if (noop) return ok();
   if (!group_end) return fail(HQ_ERR_NULL, "%s: group_end is required", what);
+  if (!aligned4(group_end)) return fail(HQ_ERR_ALIGN, "%s: group_end must be 4-byte aligned", what);
   return run_product(what, stream, p, nullptr, 0);
 }
 
@@ -254,6 +264,7 @@ hq_status hq_block_group_masked_gemm(void* stream, uint32_t flags, const uint8_t
   if ((st = check_product(what, flags, p, &noop)) != HQ_OK) return st;
   if (noop) return ok();
   if (!masked_m) return fail(HQ_ERR_NULL, "%s: masked_m is required", what);
+  if (!aligned4(masked_m)) return fail(HQ_ERR_ALIGN, "%s: masked_m must be 4-byte aligned", what);
   return run_product(what, stream, p, nullptr, 0);
 }
 
@@ -278,6 +289,7 @@ hq_status hq_block_group_k_gemm(void* stream, uint32_t flags, const uint8_t* a, 
   if ((st = check_product(what, flags, p, &noop)) != HQ_OK) return st;
   if (noop) return ok();
   if (!group_end) return fail(HQ_ERR_NULL, "%s: group_end is required", what);
+  if (!aligned4(group_end)) return fail(HQ_ERR_ALIGN, "%s: group_end must be 4-byte aligned", what);
   p.rows = m;
   p.k = k_total;
   p.nkb = (int32_t)(k_total / 128);
@@ -325,7 +337,9 @@ hq_status hq_moe_sort(void* stream, const int64_t* topk_ids, int64_t num_tokens,
   if (workspace_bytes < need)
     return fail(HQ_ERR_SHAPE, "%s: workspace_bytes=%llu, this shape needs %llu", what,
                 (unsigned long long)workspace_bytes, (unsigned long long)need);
-  if (!aligned4(workspace)) return fail(HQ_ERR_ALIGN, "%s: workspace must be 4-byte aligned", what);
+  if (!aligned8(topk_ids)) return fail(HQ_ERR_ALIGN, "%s: topk_ids must be 8-byte aligned", what);
+  if (!aligned4(row_map) || !aligned4(row_pair) || !aligned4(group_end) || !aligned4(counts) || !aligned4(workspace))
+    return fail(HQ_ERR_ALIGN, "%s: row_map, row_pair, group_end, counts and the workspace must be 4-byte aligned", what);
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_moe_sort((hipStream_t)stream, topk_ids, pairs, num_experts, align, max_rows, row_map,
@@ -350,6 +364,7 @@ hq_status hq_moe_permute(void* stream, const uint8_t* x, int64_t num_tokens, int
   if (max_rows == 0) return ok();
   if (!out || (num_tokens > 0 && (!x || !row_map))) return fail(HQ_ERR_NULL, "%s: x, row_map and out are required", what);
   if (!aligned16(x) || !aligned16(out)) return fail(HQ_ERR_ALIGN, "%s: x and out must be 16-byte aligned", what);
+  if ((st = check_index(what, row_map, group_end, counts)) != HQ_OK) return st;
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_moe_permute((hipStream_t)stream, x, num_tokens, row_bytes, row_map, topk, pad, max_rows,
@@ -376,6 +391,7 @@ hq_status hq_moe_permute_block_quant(void* stream, const uint16_t* x, int64_t nu
     return fail(HQ_ERR_NULL, "%s: x, row_map, q and sf are required", what);
   if (!aligned16(x) || !aligned16(q)) return fail(HQ_ERR_ALIGN, "%s: x and q must be 16-byte aligned", what);
   if (!aligned4(sf)) return fail(HQ_ERR_ALIGN, "%s: sf must be 4-byte aligned", what);
+  if ((st = check_index(what, row_map, group_end, counts)) != HQ_OK) return st;
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_moe_permute_block_quant((hipStream_t)stream, x, num_tokens, hidden, row_map, topk, pad,
@@ -395,6 +411,7 @@ hq_status hq_moe_combine(void* stream, const uint16_t* y, int64_t num_tokens, in
   if (!out || !row_map || (max_rows > 0 && !y)) return fail(HQ_ERR_NULL, "%s: y, row_map and out are required", what);
   if (!aligned16(y) || !aligned16(out)) return fail(HQ_ERR_ALIGN, "%s: y and out must be 16-byte aligned", what);
   if (!aligned4(weights)) return fail(HQ_ERR_ALIGN, "%s: weights must be 4-byte aligned", what);
+  if ((st = check_index(what, row_map, nullptr, nullptr)) != HQ_OK) return st;
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_moe_combine((hipStream_t)stream, y, num_tokens, hidden, row_map, topk, weights, max_rows,
@@ -421,6 +438,7 @@ hq_status hq_moe_combine_backward(void* stream, const uint16_t* dout, const uint
     return fail(HQ_ERR_ALIGN, "%s: dout, y and dy must be 16-byte aligned", what);
   if (!aligned4(weights) || !aligned4(dweights))
     return fail(HQ_ERR_ALIGN, "%s: weights and dweights must be 4-byte aligned", what);
+  if ((st = check_index(what, row_map, group_end, counts)) != HQ_OK) return st;
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_moe_combine_backward((hipStream_t)stream, dout, y, num_tokens, hidden, row_map, topk,

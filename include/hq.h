@@ -489,7 +489,7 @@ hq_status hq_block_quant(void* stream, const uint16_t* x, int64_t batch, int64_t
  * (BF16, FP16 with HQ_IN_FP16), y = up * gate / (1 + exp(-gate)) in FP32, then
  * q [rows, h], sf [rows, ceil(h/128)] as hq_block_quant in 1 x 128 blocks.
  * group_end (optional, device int32 [num_groups]): rows at or past its last
- * value are neither read nor written.  h % 32 == 0; fewer than 2^29 blocks.
+ * value are neither read nor written; 4-byte aligned.  h % 32 == 0; fewer than 2^29 blocks.
  */
 hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t rows,
                                       int64_t h, const int32_t* group_end,
@@ -513,7 +513,8 @@ hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t r
  *   a [.., k] codes, sfa [.., ceil(k/128)] (1 x 128 blocks);
  *   b [.., n, k] codes, sfb [.., ceil(n/128), ceil(k/128)] (128 x 128 blocks).
  * k % 32 == 0, n % 8 == 0, 256 k < 2^31; a, b, out and the workspace 16-byte
- * aligned, scales 4-byte aligned.  m == 0 or n == 0 is a no-op.
+ * aligned, scales and the groups' ends and counts 4-byte aligned.  m == 0 or
+ * n == 0 is a no-op.
  * Gradients: with W [n, k] and dY [m, n], the gradient for X [m, k] is the
  * product of dY's row codes with W's HQ_BLOCK_2D | HQ_TRANSPOSE codes, and the
  * gradient for W that of dY's HQ_TRANSPOSE codes with X's
@@ -579,8 +580,9 @@ hq_status hq_block_group_k_gemm(void* stream, uint32_t flags, const uint8_t* a,
  * max_rows is at least the most rows that any ids can take,
  * (P + min(num_experts, P) (align - 1)) / align * align for P = num_tokens *
  * topk (HQ_ERR_SHAPE otherwise).  1 <= num_experts, align <= 1024.  The
- * workspace (4-byte aligned) holds hq_moe_sort_workspace_size bytes, never
- * more than HQ_SORT_WORKSPACE_BYTES; it may be NULL where that is 0.
+ * workspace holds hq_moe_sort_workspace_size bytes, never more than
+ * HQ_SORT_WORKSPACE_BYTES; it may be NULL where that is 0.  It and the int32
+ * tensors are 4-byte aligned, topk_ids 8-byte.
  */
 #define HQ_SORT_WORKSPACE_BYTES (1u << 20)
 hq_status hq_moe_sort(void* stream, const int64_t* topk_ids, int64_t num_tokens,
