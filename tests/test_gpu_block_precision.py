@@ -50,3 +50,49 @@ def test_group_k_keeps_fp32_sums(blocks, m, n, dtype):
         lo, hi = int(ends[g]) - 128 * blocks[g], int(ends[g])
         ref, mag = B.gemm(a[:, lo:hi], sa[:, lo // 128:hi // 128], b[:, lo:hi], sb[:, lo // 128:hi // 128])
         H.check(out[g], ref, H.product_bound(ref, mag, max(hi - lo, 1), dtype), f"{what} group {g}")
+
+
+def _kept(ref, mag, k, dtype, fp8):
+    """The documented bound: an FP32 sum rounded once, and where the FP8 matrix
+    instructions make the inner sums less than 2^-10 of their magnitudes on top
+    (eight products of which seven lose up to 2^-13 of the largest)."""
+    return H.product_bound(ref, mag, k, dtype) + (2.0 ** -10 * mag if fp8 else 0.0)
+
+
+@pytest.mark.parametrize("m,n,k", [(8, 136, 1024), (16, 264, 2080), (24, 136, 512), (40, 264, 1056), (300, 520, 768),
+                                   (72, 392, 384), (520, 1032, 640)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_dense_keeps_what_is_documented(m, n, k, dtype):
+    """Only BF16 results of more than 16 rows and k >= 512 may use the FP8
+    instructions; the others keep FP32 sums.  With and without a K split."""
+    what = f"dense precision {m}x{n}x{k} {dtype}"
+    U.banner(what)
+    a, sa, b, sb = _straining(H.rng(what), m, n, k)
+    ref, mag = B.gemm(a, sa, b, sb)
+    bound = _kept(ref, mag, k, dtype, dtype is BF16 and m > 16 and k >= 512)
+    for ws in (None, torch.empty(hq.HQ_BLOCK_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")):
+        out = torch.full((m, n), float("nan"), dtype=dtype, device="cuda")
+        hq.hq_block_gemm(*[H.dev(v) for v in (a, sa, b, sb)], out, workspace=ws)
+        H.check(out, ref, bound, what)
+
+
+@pytest.mark.parametrize("per,k", [(24, 512), (100, 1056), (400, 640), (60, 384)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_groups_keep_what_is_documented(per, k, dtype):
+    """Contiguous groups and masked slots of `per` rows: BF16 results of k >= 512
+    may use the FP8 instructions."""
+    what = f"group precision {per} rows k={k} {dtype}"
+    U.banner(what)
+    r = H.rng(what)
+    E, n = 3, 264
+    a, sa, _, _ = _straining(r, E * per, n, k)
+    W = [_straining(r, 8, n, k)[2:] for _ in range(E)]
+    args = (H.dev(a), H.dev(sa), H.dev(np.stack([w[0] for w in W])), H.dev(np.stack([w[1] for w in W])))
+    outs = [torch.full((E * per, n), float("nan"), dtype=dtype, device="cuda") for _ in range(2)]
+    hq.hq_block_group_contiguous_gemm(*args, U.dev_i32(per * np.arange(1, E + 1), "cuda"), outs[0])
+    hq.hq_block_group_masked_gemm(*args, U.dev_i32([per] * E, "cuda"), outs[1], per)
+    for g in range(E):
+        rows = slice(g * per, (g + 1) * per)
+        ref, mag = B.gemm(a[rows], sa[rows], *W[g])
+        for out in outs:
+            H.check(out[rows], ref, _kept(ref, mag, k, dtype, dtype is BF16 and k >= 512), f"{what} group {g}")
