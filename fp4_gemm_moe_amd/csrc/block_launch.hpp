@@ -1,15 +1,13 @@
-// Host side of the tiled block-128 FP8 GEMM: tile shapes and launches.
+// Host side of the tiled block-128 FP8 GEMM: launches.
 #pragma once
 
 #include <atomic>
 #include <type_traits>
 
+#include "block_plan.hpp"
 #include "block_tiled.hpp"
 
 namespace hq {
-
-// Tile shapes of the tiled kernel (rows x columns).
-enum BlockTile : int { kTile256x256, kTile256x128, kTile128x256, kTile128x128, kTile64x128 };
 
 hipError_t launch_block_fast(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, int policy);
 hipError_t launch_block_exact(hipStream_t s, const BlockGemmArgs& p, const DeviceInfo& dev, int tile, int policy);
