@@ -73,19 +73,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_
 // at voff + soff: lane j's result lands at LDS address lds + j * size.  In
 // inline assembly, so that the compiler adds no waits of its own; the kernel
 // waits on the vector-memory counter and a barrier before a stage is read.  m0
-// is set inside each statement and used by nothing else.
+// is set inside each statement and used by nothing else; the load needs one
+// wait state after that, which the compiler does not add inside a statement.
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(r), "s"(soff), "s"(lds)
-               : "memory");
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               ::"v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory");
 }
 // The same for bytes that one workgroup reads once (non-temporal policy).
 __device__ __forceinline__ void dma16nt(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds" ::"v"(voff), "s"(r), "s"(soff), "s"(lds)
-               : "memory");
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+               ::"v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory");
 }
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(r), "s"(soff), "s"(lds)
-               : "memory");
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+               ::"v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory");
 }
 
 template <int N>

@@ -80,9 +80,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base, int6
 // orders these writes explicitly (a wait on the vector-memory counter, then a
 // workgroup barrier, before a stage is read; a barrier after the last read of
 // a stage before it is refilled).  m0 is set inside each statement; nothing
-// else in the kernel uses it.
+// else in the kernel uses it.  The load needs one wait state after a scalar
+// write of m0, which the compiler does not add inside a statement.
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(r),
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(r),
                "s"(lds) : "memory");
 }
 // The same with the non-temporal cache policy, for operands read exactly
@@ -90,11 +91,11 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, u
 // (256 rows x 128 bytes per step, one workgroup per CU) reads 7.0 TB/s with
 // it and 4.6 TB/s without.
 __device__ __forceinline__ void dma16nt(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(voff), "s"(r),
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(voff), "s"(r),
                "s"(lds) : "memory");
 }
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(r),
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(r),
                "s"(lds) : "memory");
 }
 
