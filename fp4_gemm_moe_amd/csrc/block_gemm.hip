@@ -21,8 +21,12 @@ namespace {
 // blocks in flight), and their sums meet in LDS in wave order.  No LDS staging:
 // a row's 128 codes are read once, in the lanes that multiply them.  Every wave
 // that fits keeps loads under way: W = 16, U = 2 was the best of W 4 .. 16, U 1 ..
-// 4 (1x17408x5120 17.6 us, 5.1 TB/s of weights, a large copy's rate; 16 rows of
-// A from the L2s take it to 26 us).  Non-temporal weight loads cost 1 to 17 %.
+// 4.  1x17408x5120 takes 17.4 us where a part of the 89 MB of weights is still in
+// the Infinity Cache (three sets of operands in turn), 20.2 us, 4.4 TB/s, where
+// none is.  With more rows every workgroup's reads of A from the L2s and the
+// widening of both operands show: 16 rows 27 and 30.5 us.  Narrow outputs leave
+// units without work (1x1536x7168 6.6 us, 1.7 TB/s).  Non-temporal weight loads
+// cost 1 to 17 %.
 template <int MF, int NF, int W, int U>
 __global__ __launch_bounds__(W * 64) void block_gemm_direct(BlockGemmArgs p) {
   __shared__ v4f part[W - 1][MF * NF][64];

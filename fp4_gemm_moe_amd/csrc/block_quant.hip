@@ -3,9 +3,17 @@
 // transposed, and the SwiGLU of a gate|up row quantised in 1 x 128 blocks.
 //
 // Every form reads its input once and writes codes and scales once: 3 bytes
-// an element (5 for SwiGLU outputs), so memory bounds them: [65536, 4096] rows
-// 805 MB in 132 to 138 us, 5.8 to 6.1 TB/s (a large copy reaches 5.1); 32 x
-// [4096, 1536] in 128 x 128 blocks 604 MB in 109 us, transposed in 103 to 110.
+// an element (5 for SwiGLU outputs).  A large copy reaches 5.1 TB/s.  Memory
+// bounds the row form, also with partial blocks, SwiGLU, and tiles whose rows are
+// whole lines of x and q: [65536, 4096] rows 132 us, 6.2 TB/s; SwiGLU of [65536, 2 x
+// 1536] 90 us, 5.6; 32 x [4096, 1536] in 128 x 128 blocks 109 us, transposed 103.
+// Tiles fall behind it otherwise: a tile row's 256 bytes of x straddle lines
+// where k % 64 != 0, and a row's 128 bytes of codes are parts of lines where q's
+// rows are not a multiple of 128 bytes ([16416, 4128] against [16384, 4096], us: 128 x
+// 128 50.8, 39.7; transposed 48.3, 41.4; 1 x 128 transposed 52.2, 42.0); 1 x 128
+// transposed also writes its scales one by one into as many lines ([65536, 4096]
+// 181 us, 4.5 TB/s).  Up to about 20 MB launch and latency are half of the time
+// ([4096, 1536] 6 to 7 us for 3.7).
 #include "block_fmt.hpp"
 #include "block_internal.hpp"
 

@@ -25,11 +25,11 @@
 // V_MFMA_F32_16X16X32_F16 at half the rate, with full FP32 sums.
 //
 // What bounds it: the matrix cores, at the clock that they leave.  Contiguous
-// groups, 65536 rows x 3072 x 4096: 795 us, 2.07 PFLOP/s; the matrix cores work
-// 57 % of the cycles, the additions (half as many issue cycles as the matrix
+// groups, 65536 rows x 3072 x 4096: 770 to 800 us over several cards, 2.06 to
+// 2.14 PFLOP/s; the matrix cores work 56 % of the cycles, the additions (half as many issue cycles as the matrix
 // instructions) and the fragments' LDS reads fill most of the others, and the
 // clock falls to 1.6 - 1.8 GHz of 2.4.  FP32 results of 65536 rows in 32 K groups,
-// 4096 x 1536, through FP16: 850 to 880 us, 0.94 to 0.97 PFLOP/s.
+// 4096 x 1536, through FP16: 845 to 910 us, 0.91 to 0.98 PFLOP/s.
 // Measured against it (the contiguous case unless said): 32 x 32 fragments in
 // the same form 5 % slower; row / 8 swizzles as for 32-row fragments 3 %; loads
 // spread over the whole step 1 to 4 %; two workgroups a compute unit with two

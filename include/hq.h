@@ -502,8 +502,9 @@ hq_status hq_fused_swiglu_block_quant(void* stream, const uint16_t* x, int64_t r
  *               * sum over k in kb of a[r, k] b[n, k]
  * the inner sums on the matrix cores and the outer one in FP32, rounded once
  * to BF16 (FP16 with HQ_OUT_FP16; kept in FP32 with HQ_OUT_FP32; added in
- * FP32 to out with HQ_OUT_FP32 | HQ_ACCUMULATE).  A product of two scales
- * has to be a finite FP32 number.
+ * FP32 to out with HQ_OUT_FP32 | HQ_ACCUMULATE).  The two scales are
+ * multiplied in FP32: their product has to be finite, and where it is below
+ * 2^-126 the block loses precision with it.
  * Precision of the inner sums: FP16 and FP32 results, any result of k < 512 and
  * all of hq_block_group_k_gemm multiply the codes exactly and add in FP32.
  * Other BF16 results use the FP8 matrix instructions, which align eight
