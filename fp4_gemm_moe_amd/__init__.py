@@ -31,6 +31,9 @@ __all__ = [
     "hq_block_group_k_gemm", "hq_moe_sort", "hq_moe_sort_workspace_size", "hq_moe_permute",
     "hq_moe_permute_block_quant", "hq_moe_combine", "hq_moe_combine_backward",
     "block_quantize", "moe_max_rows", "moe_sort",
+    "hq_half_group_contiguous_gemm", "hq_half_group_masked_gemm", "hq_half_group_k_gemm", "hq_swiglu",
+    "hq_swiglu_backward", "hq_lora", "hq_lora_workspace_size", "hq_lora_backward",
+    "hq_lora_backward_workspace_size", "lora_plan",
     "hq_last_error", "library_path", "load", "EXPORTED_SYMBOLS",
     "quantize", "group_size", "code_cols",
 ]
@@ -64,6 +67,9 @@ EXPORTED_SYMBOLS = (
     "hq_block_group_contiguous_gemm", "hq_block_group_masked_gemm", "hq_block_group_k_gemm",
     "hq_moe_sort", "hq_moe_sort_workspace_size", "hq_moe_permute", "hq_moe_permute_block_quant",
     "hq_moe_combine", "hq_moe_combine_backward",
+    "hq_half_group_contiguous_gemm", "hq_half_group_masked_gemm", "hq_half_group_k_gemm",
+    "hq_swiglu", "hq_swiglu_backward", "hq_lora", "hq_lora_workspace_size", "hq_lora_backward",
+    "hq_lora_backward_workspace_size",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -128,6 +134,17 @@ _SIGS = {
     "hq_moe_combine": ([_VP, _VP, _I64, _I64, _VP, _I32, _VP, _I64, _VP, _U32], _I32),
     "hq_moe_combine_backward": ([_VP, _VP, _VP, _I64, _I64, _VP, _I32, _VP, _VP, _VP, _I32, _I64, _VP, _VP,
                                  _U32], _I32),
+    "hq_half_group_contiguous_gemm": ([_VP, _U32, _VP, _VP, _VP, _I32, _VP, _I64, _I64, _I64], _I32),
+    "hq_half_group_masked_gemm": ([_VP, _U32, _VP, _VP, _VP, _I32, _I64, _VP, _I64, _I64], _I32),
+    "hq_half_group_k_gemm": ([_VP, _U32, _VP, _VP, _VP, _I32, _VP, _I64, _I64, _I64], _I32),
+    "hq_swiglu": ([_VP, _VP, _I64, _I64, _I32, _VP, _I64, _VP, _VP, _U32], _I32),
+    "hq_swiglu_backward": ([_VP, _VP, _VP, _I64, _I64, _I32, _VP, _I64, _VP, _VP, _VP, _U32], _I32),
+    "hq_lora": ([_VP, _U32, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I64, _VP, _VP, _VP, _I64, _I64, _I64, _I64,
+                 _VP, _U64], _I32),
+    "hq_lora_workspace_size": ([_I64, _I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_uint64)], _I32),
+    "hq_lora_backward": ([_VP, _U32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _I64, _VP, _VP, _VP, _VP,
+                          _I64, _I64, _I64, _I64, _VP, _U64], _I32),
+    "hq_lora_backward_workspace_size": ([_I64, _I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_uint64)], _I32),
 }
 
 
@@ -804,6 +821,206 @@ def moe_sort(topk_ids, num_experts, align=1):
     ws = torch.empty(hq_moe_sort_workspace_size(T, topk, num_experts), dtype=torch.uint8, device=dev)
     hq_moe_sort(topk_ids, num_experts, align, row_map, row_pair, group_end, counts, ws)
     return row_map, row_pair, group_end, counts
+
+
+# ---------------------------------------------------------------- 16-bit products by expert
+class _Call:
+    """One call's tensors: their addresses, checked like _arg's, all of one device.
+    Entered, it makes that device the current one, which the library launches on."""
+
+    def __init__(self, first):
+        self.device = first.get_device()
+        if self.device < 0:
+            raise ValueError("tensors must be device tensors")
+
+    def arg(self, t, name, dtype, shape):
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device or not t.is_contiguous():
+            _need(t, name, dtype)
+            if t.get_device() != self.device:
+                raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors on cuda:{self.device}")
+            raise ValueError(f"{name} has the shape {tuple(t.shape)}, expected {tuple(shape)}")
+        return t.data_ptr()
+
+    def opt(self, t, name, dtype, shape):
+        return None if t is None else self.arg(t, name, dtype, shape)
+
+    def workspace(self, t):
+        if t is None:
+            return None, 0
+        if t.get_device() != self.device or not t.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+        return t.data_ptr(), t.numel() * t.element_size()
+
+    def run(self, fn, *args):
+        """fn(the device's current stream, *args)."""
+        if self.device == torch.cuda.current_device():
+            _check(fn(torch._C._cuda_getCurrentRawStream(self.device), *args))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(torch._C._cuda_getCurrentRawStream(self.device), *args))
+
+
+def _half_dtype(t, name):
+    if t.dtype not in _HALVES:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return t.dtype
+
+
+def _half_product(a, out, transpose, accumulate):
+    """The operands' type and the flags of a 16-bit product."""
+    dt = _half_dtype(a, "a")
+    if out.dtype is not dt and out.dtype is not torch.float32:
+        raise ValueError(f"out must be {dt} or float32, got {out.dtype}")
+    if accumulate and out.dtype is not torch.float32:
+        raise ValueError("accumulate needs a float32 out")
+    return dt, (_in_flag(a) | (HQ_TRANSPOSE if transpose else 0) | (HQ_OUT_FP32 if out.dtype is torch.float32 else 0)
+                | (HQ_ACCUMULATE if accumulate else 0))
+
+
+def hq_half_group_contiguous_gemm(a, b, group_end, out, transpose=False, accumulate=False):
+    """out[r] = a[r] b[g]^T for the rows r in [group_end[g-1], group_end[g]): a
+    [rows, k] and b [E, n, k] bfloat16 or float16, out [rows, n] of that type or
+    float32 (accumulate: out += the product).  With transpose b is [E, k, n] and
+    out[r] = a[r] b[g]: the gradient for the activations.  Rows past the last end
+    are left alone."""
+    c = _Call(a)
+    dt, flags = _half_product(a, out, transpose, accumulate)
+    rows, k = a.shape
+    E, n = b.shape[0], b.shape[2 if transpose else 1]
+    c.run(load().hq_half_group_contiguous_gemm, flags, c.arg(a, "a", dt, (rows, k)),
+          c.arg(b, "b", dt, (E, k, n) if transpose else (E, n, k)), c.arg(group_end, "group_end", torch.int32, (E,)), E,
+          c.arg(out, "out", out.dtype, (rows, n)), rows, n, k)
+
+
+def hq_half_group_masked_gemm(a, b, masked_m, out, max_m, transpose=False, accumulate=False):
+    """The same for expert e's first masked_m[e] rows of slot [e*max_m, (e+1)*max_m)."""
+    c = _Call(a)
+    dt, flags = _half_product(a, out, transpose, accumulate)
+    rows, k = a.shape
+    E, n = b.shape[0], b.shape[2 if transpose else 1]
+    if rows != E * max_m:
+        raise ValueError(f"a has {rows} rows, expected num_groups * max_m = {E * max_m}")
+    c.run(load().hq_half_group_masked_gemm, flags, c.arg(a, "a", dt, (rows, k)),
+          c.arg(b, "b", dt, (E, k, n) if transpose else (E, n, k)), c.arg(masked_m, "masked_m", torch.int32, (E,)), E,
+          max_m, c.arg(out, "out", out.dtype, (rows, n)), n, k)
+
+
+def hq_half_group_k_gemm(a, b, group_end, out, accumulate=False):
+    """out[g] = sum over the rows r in [group_end[g-1], group_end[g]) of a[r]^T b[r]:
+    a [rows, m] and b [rows, n] bfloat16 or float16, out [E, m, n] of that type or
+    float32 -- the gradient for the weights, from a product's operands as they are."""
+    c = _Call(a)
+    dt, flags = _half_product(a, out, False, accumulate)
+    rows, m = a.shape
+    n, E = b.shape[1], group_end.numel()
+    c.run(load().hq_half_group_k_gemm, flags, c.arg(a, "a", dt, (rows, m)), c.arg(b, "b", dt, (rows, n)),
+          c.arg(group_end, "group_end", torch.int32, (E,)), E, c.arg(out, "out", out.dtype, (E, m, n)), m, n, rows)
+
+
+def _selection(c, rows, num_groups, group_end, slot_rows, valid):
+    if group_end is not None and num_groups == 0:
+        num_groups = group_end.numel()
+    return (num_groups, c.opt(group_end, "group_end", torch.int32, (num_groups,)), slot_rows,
+            c.opt(valid, "valid", torch.int32, (num_groups,)))
+
+
+def hq_swiglu(x, y, num_groups=0, group_end=None, slot_rows=0, valid=None):
+    """y [rows, h] = up * gate * sigmoid(gate) for x [rows, 2h] = [gate | up],
+    bfloat16 or float16.  All rows, or by group as in hq_fused_swiglu_quant: those
+    up to group_end [num_groups], or slots of slot_rows, and of each group the first
+    valid[g].  Other rows are left alone."""
+    c = _Call(x)
+    dt = _half_dtype(x, "x")
+    rows, h = x.shape[0], x.shape[1] // 2
+    sel = _selection(c, rows, num_groups, group_end, slot_rows, valid)
+    c.run(load().hq_swiglu, c.arg(x, "x", dt, (rows, 2 * h)), rows, h, *sel, c.arg(y, "y", dt, (rows, h)), _in_flag(x))
+
+
+def hq_swiglu_backward(dy, x, dx, y=None, num_groups=0, group_end=None, slot_rows=0, valid=None):
+    """The gradient dx [rows, 2h] of hq_swiglu for dy [rows, h], and y once more
+    where it is given.  dx may be x, and y may be dy."""
+    c = _Call(x)
+    dt = _half_dtype(x, "x")
+    rows, h = x.shape[0], x.shape[1] // 2
+    sel = _selection(c, rows, num_groups, group_end, slot_rows, valid)
+    c.run(load().hq_swiglu_backward, c.arg(dy, "dy", dt, (rows, h)), c.arg(x, "x", dt, (rows, 2 * h)), rows, h, *sel,
+          c.arg(dx, "dx", dt, (rows, 2 * h)), c.opt(y, "y", dt, (rows, h)), _in_flag(x))
+
+
+# ---------------------------------------------------------------- low-rank adapters
+def _lora_size(fn, m, n, k, r, adapters, max_rows):
+    out = ctypes.c_uint64(0)
+    _check(fn(m if max_rows is None else max_rows, n, k, r, adapters, ctypes.byref(out)))
+    return int(out.value)
+
+
+def hq_lora_workspace_size(m, n, k, r, adapters, max_rows=None):
+    """Bytes of workspace hq_lora needs for m tokens (max_rows places: m by default)."""
+    return _lora_size(load().hq_lora_workspace_size, m, n, k, r, adapters, max_rows)
+
+
+def hq_lora_backward_workspace_size(m, n, k, r, adapters, max_rows=None):
+    """Bytes of workspace hq_lora_backward needs for m tokens."""
+    return _lora_size(load().hq_lora_backward_workspace_size, m, n, k, r, adapters, max_rows)
+
+
+def _lora_plan(c, m, L, row_map, row_pair):
+    if (row_map is None) != (row_pair is None):
+        raise ValueError("row_map and row_pair go together")
+    if row_pair is None:
+        return None, None, m
+    places = row_pair.numel()
+    if row_map.dim() == 2:                     # as hq_moe_sort has it, with topk 1
+        row_map = row_map[:, 0]
+    return c.arg(row_map, "row_map", torch.int32, (m,)), c.arg(row_pair, "row_pair", torch.int32, (places,)), places
+
+
+def hq_lora(x, a, b, scale, group_end, out, base=None, row_map=None, row_pair=None, v=None, workspace=None):
+    """out[t] = base[t] + scale[g] (x[t] a[g]^T) b[g]^T for token t's adapter g: x
+    [m, k], a [L, r, k], b [L, n, r], base and out [m, n] bfloat16 or float16, scale
+    float32 [L] or None (1).  group_end, row_map and row_pair are hq_moe_sort's for
+    the tokens' adapters (lora_plan); without row_map and row_pair the tokens lie
+    in the order of their adapters.  Tokens without an adapter get base's rows
+    (zeros without a base, and are left alone where base is out).  v float32
+    [places, r] keeps x a^T for the gradients."""
+    c = _Call(x)
+    dt = _half_dtype(x, "x")
+    m, k = x.shape
+    L, r = a.shape[:2]
+    n = b.shape[1]
+    mp, pp, places = _lora_plan(c, m, L, row_map, row_pair)
+    wp, wb = c.workspace(workspace)
+    c.run(load().hq_lora, _in_flag(x), c.arg(x, "x", dt, (m, k)), c.arg(a, "a", dt, (L, r, k)),
+          c.arg(b, "b", dt, (L, n, r)), c.opt(scale, "scale", torch.float32, (L,)),
+          c.arg(group_end, "group_end", torch.int32, (L,)), L, mp, pp, places, c.opt(base, "base", dt, (m, n)),
+          c.arg(out, "out", dt, (m, n)), c.opt(v, "v", torch.float32, (places, r)), m, n, k, r, wp, wb)
+
+
+def hq_lora_backward(dy, x, v, a, b, scale, group_end, da, db, dx=None, base=None, row_map=None, row_pair=None,
+                     accumulate=False, workspace=None):
+    """The gradients of hq_lora for dy [m, n]: dx [m, k] = base + the adapters' share
+    (base: the gradient for x through the projection; dx None: not computed), da
+    float32 [L, r, k] and db float32 [L, n, r] (accumulate: added to them)."""
+    c = _Call(x)
+    dt = _half_dtype(x, "x")
+    m, k = x.shape
+    L, r = a.shape[:2]
+    n = b.shape[1]
+    mp, pp, places = _lora_plan(c, m, L, row_map, row_pair)
+    wp, wb = c.workspace(workspace)
+    c.run(load().hq_lora_backward, _in_flag(x) | (HQ_ACCUMULATE if accumulate else 0), c.arg(dy, "dy", dt, (m, n)),
+          c.arg(x, "x", dt, (m, k)), c.arg(v, "v", torch.float32, (places, r)), c.arg(a, "a", dt, (L, r, k)),
+          c.arg(b, "b", dt, (L, n, r)), c.opt(scale, "scale", torch.float32, (L,)),
+          c.arg(group_end, "group_end", torch.int32, (L,)), L, mp, pp, places, c.opt(base, "base", dt, (m, k)),
+          c.opt(dx, "dx", dt, (m, k)), c.arg(da, "da", torch.float32, (L, r, k)),
+          c.arg(db, "db", torch.float32, (L, n, r)), m, n, k, r, wp, wb)
+
+
+def lora_plan(adapter_ids, num_adapters):
+    """The plan of a batch for hq_lora, from its tokens' adapters (int64 [m], -1:
+    none): (group_end, row_map, row_pair), allocated with torch."""
+    row_map, row_pair, group_end, _ = moe_sort(adapter_ids.view(-1, 1), num_adapters)
+    return group_end, row_map.view(-1), row_pair
 
 
 # ---------------------------------------------------------------- allocation helper

@@ -641,6 +641,130 @@ hq_status hq_moe_combine_backward(void* stream, const uint16_t* dout, const uint
                                   int64_t max_rows, uint16_t* dy, float* dweights,
                                   uint32_t flags);
 
+/* ------------------------------------------------------------------------
+ * 16-bit products by expert
+ * ------------------------------------------------------------------------
+ * Operands of BF16 (FP16 with HQ_IN_FP16) values, multiplied exactly and summed
+ * in FP32 on the matrix cores.  out holds the operands' type, rounded once to
+ * nearest even; FP32 with HQ_OUT_FP32; with HQ_OUT_FP32 | HQ_ACCUMULATE the
+ * product is added to it in FP32.  n % 8 == 0, k % 8 == 0 (m % 8 == 0 where a
+ * is [rows, m]); n, k and that m below 2^21; a, b and out 16-byte aligned, the
+ * groups' ends and counts 4-byte aligned.  No rows or n == 0 is a no-op.  Rows
+ * that belong to no group are not read into a result and not written.
+ *
+ * hq_half_group_contiguous_gemm: out[r] = a[r] b[g]^T for the rows r of group
+ *   g, as hq_group_contiguous_gemm has them (ends clamped to non-decreasing ones
+ *   in [0, m_total]); a [m_total, k], b [num_groups, n, k], out [m_total, n].
+ *   With HQ_TRANSPOSE b is [num_groups, k, n] and out[r] = a[r] b[g]: with the
+ *   weights W [n', k'] of a forward product as they are, the gradient for its
+ *   activations is the product of their gradient [m_total, n'] with W.
+ * hq_half_group_masked_gemm: the same over padded slots, as
+ *   hq_group_masked_gemm (counts clamped to [0, max_m_per_group]).
+ * hq_half_group_k_gemm: out[g] = sum over the rows r of group g of a[r]^T b[r];
+ *   a [rows, m], b [rows, n], out [num_groups, m, n]: the gradient for the
+ *   weights of a contiguous product, from its operands as they are.  Groups may
+ *   have any size; one without rows gives zeros (leaves out as it is with
+ *   HQ_ACCUMULATE).
+ */
+hq_status hq_half_group_contiguous_gemm(void* stream, uint32_t flags, const uint16_t* a,
+                                        const uint16_t* b, const int32_t* group_end,
+                                        int32_t num_groups, void* out, int64_t m_total,
+                                        int64_t n, int64_t k);
+hq_status hq_half_group_masked_gemm(void* stream, uint32_t flags, const uint16_t* a,
+                                    const uint16_t* b, const int32_t* masked_m,
+                                    int32_t num_groups, int64_t max_m_per_group, void* out,
+                                    int64_t n, int64_t k);
+hq_status hq_half_group_k_gemm(void* stream, uint32_t flags, const uint16_t* a,
+                               const uint16_t* b, const int32_t* group_end,
+                               int32_t num_groups, void* out, int64_t m, int64_t n,
+                               int64_t rows);
+
+/*
+ * SwiGLU that stays in 16 bits, and its gradient: x [rows, 2h] = [gate | up]
+ * (BF16, FP16 with HQ_IN_FP16), s = 1 / (1 + exp(-gate)),
+ *   y     = up gate s                               [rows, h]
+ *   dgate = dy up s (1 + gate (1 - s)),  dup = dy gate s,  dx = [dgate | dup]
+ * in FP32, rounded once.  The gradient also writes y again where y is not NULL
+ * (the operand of the down projection's weights' gradient, which then need not
+ * be kept).
+ * Row selection as in hq_fused_swiglu_quant, with num_groups == 0 (group_end and
+ * valid NULL) for all rows; rows that are not selected are neither read nor
+ * written.  h % 8 == 0, h < 2^27; x, y, dy and dx 16-byte aligned, group_end and
+ * valid 4-byte aligned.  dx may be x, and y of the gradient may be dy.  One
+ * launch takes fewer than 2^35 values of y.
+ */
+hq_status hq_swiglu(void* stream, const uint16_t* x, int64_t rows, int64_t h,
+                    int32_t num_groups, const int32_t* group_end, int64_t slot_rows,
+                    const int32_t* valid, uint16_t* y, uint32_t flags);
+hq_status hq_swiglu_backward(void* stream, const uint16_t* dy, const uint16_t* x,
+                             int64_t rows, int64_t h, int32_t num_groups,
+                             const int32_t* group_end, int64_t slot_rows,
+                             const int32_t* valid, uint16_t* dx, uint16_t* y,
+                             uint32_t flags);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests at once
+ * ------------------------------------------------------------------------
+ * Beside any projection of this library (or another one): token t of a batch has
+ * the adapter g, or none,
+ *   out[t] = base[t] + scale[g] (x[t] A[g]^T) B[g]^T
+ *   x, base, out  [m, k], [m, n], [m, n] BF16 (FP16 with HQ_IN_FP16)
+ *   a, b          [num_adapters, r, k], [num_adapters, n, r] of the same type
+ *   scale         [num_adapters] FP32 (NULL: 1)
+ * Sums are FP32; x A^T keeps FP32, and the product with B takes it to at least
+ * 16 bits (of each value, for BF16; of the largest in the token's row, for
+ * FP16); out is rounded once.  An adapter of a smaller rank holds zeros in the
+ * rest of its rows of A or columns of B.
+ * base NULL counts as zeros.  Tokens without an adapter get base's row (zeros
+ * without base); where base is out, they are not touched.
+ *
+ * The plan is hq_moe_sort's with topk 1 and the tokens' adapters as ids (-1, or
+ * any other id outside [0, num_adapters), for none), made once for all layers of
+ * a batch: group_end [num_adapters], row_map [m], row_pair [max_rows].  row_map
+ * and row_pair may both be NULL, with max_rows == m, where the tokens already
+ * lie in the order of their adapters: those from group_end[g - 1] to
+ * group_end[g] have g, those past the last end none.  Ends are clamped to
+ * non-decreasing ones in [0, max_rows], entries of row_pair outside [0, m) hold
+ * no token and those of row_map outside [0, the last end) no place; no token may
+ * have two places.
+ *   v  [max_rows, r] FP32 (NULL: not kept): x A^T by place, which the gradients
+ *      need; places without a token are not written.
+ * r % 8 == 0, 8 <= r <= 512; n % 8 == 0, k % 8 == 0, both below 2^21 and
+ * positive; max_rows < 2^31; 1 <= num_adapters <= 1024.  The workspace holds
+ * hq_lora_workspace_size bytes; two calls in flight need two.  16-bit tensors,
+ * v, da, db and the workspace are 16-byte aligned, the others 4-byte.  m == 0
+ * writes nothing but, in the gradient, da and db.
+ *
+ * hq_lora_backward: for dy, the gradient of out, and u[t] = dy[t] B[g],
+ *   dx[t] = base[t] + scale[g] u[t] A[g]
+ *   da[g] = scale[g] sum over g's tokens of u[t]^T x[t]      [num_adapters, r, k] FP32
+ *   db[g] = scale[g] sum over g's tokens of dy[t]^T v[t]     [num_adapters, n, r] FP32
+ * base [m, k] is the gradient for x through the projection, read and written as
+ * above (it may be dx); dx NULL: it is not computed (base is then NULL too).  With
+ * HQ_ACCUMULATE da and db are added to.  An adapter without tokens gets zeros (is
+ * left as it is).  The sums' order is fixed: results do not vary from run to run.
+ * The workspace holds hq_lora_backward_workspace_size bytes.
+ */
+hq_status hq_lora(void* stream, uint32_t flags, const uint16_t* x, const uint16_t* a,
+                  const uint16_t* b, const float* scale, const int32_t* group_end,
+                  int32_t num_adapters, const int32_t* row_map, const int32_t* row_pair,
+                  int64_t max_rows, const uint16_t* base, uint16_t* out, float* v,
+                  int64_t m, int64_t n, int64_t k, int64_t r, void* workspace,
+                  uint64_t workspace_bytes);
+hq_status hq_lora_workspace_size(int64_t max_rows, int64_t n, int64_t k, int64_t r,
+                                 int32_t num_adapters, uint64_t* bytes);
+hq_status hq_lora_backward(void* stream, uint32_t flags, const uint16_t* dy,
+                           const uint16_t* x, const float* v, const uint16_t* a,
+                           const uint16_t* b, const float* scale,
+                           const int32_t* group_end, int32_t num_adapters,
+                           const int32_t* row_map, const int32_t* row_pair,
+                           int64_t max_rows, const uint16_t* base, uint16_t* dx,
+                           float* da, float* db, int64_t m, int64_t n, int64_t k,
+                           int64_t r, void* workspace, uint64_t workspace_bytes);
+hq_status hq_lora_backward_workspace_size(int64_t max_rows, int64_t n, int64_t k,
+                                          int64_t r, int32_t num_adapters,
+                                          uint64_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif
