@@ -2,6 +2,8 @@
 // instantiate it).
 #pragma once
 
+#include <utility>
+
 #include "block_gemm.hpp"
 #include "half_internal.hpp"
 #include "tile_util.hpp"
@@ -29,19 +31,31 @@ __device__ __forceinline__ void mfma(v4f& acc, v4i a, v4i b) {
   }
 }
 
+// f(0), .., f(N - 1) with the numbers as constants (the compiler gives up
+// unrolling loops of this size).
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+  each_of(f, std::make_integer_sequence<int, N>());
+}
+
 template <int BM_, int BN_, int WM_, int WN_, int ST_>
 struct Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int WTM = BM / WM, WTN = BN / WN, FI = WTM / 16, FJ = WTN / 16;
-  static constexpr int AL = BM / 8 / WAVES, BL = BN / 8 / WAVES;   // loads a wave, per step
+  static constexpr int AL = BM / 8 / WAVES, BL = BN / 8 / WAVES;   // loads a wave, per step of 64 K values
   static constexpr int STAGE = (BM + BN) * 128;
-  static constexpr bool AGPR = FI * FJ >= 64;        // sums that take half of the register file
+  static constexpr bool BIG = FI * FJ >= 64;        // sums that take half of the register file
   // the epilogue's share of a wave: 16 rows of at most 256 bytes, padded
   static constexpr int EROW = WTN * 2 < 256 ? WTN * 2 : 256, ESTRIDE = EROW + 16, ESHARE = 16 * ESTRIDE;
   static constexpr int SMEM = ST * STAGE + WAVES * ESHARE;
   static_assert(BM / 8 % WAVES == 0 && BN / 8 % WAVES == 0 && AL >= 1 && BL >= 1, "whole loads");
   static_assert(WAVES % 2 == 0, "the row swizzle's period");
+  static_assert((AL + BL) * (ST - 1) <= 63, "the vector-memory counter");
 };
 
 struct Table {
@@ -56,10 +70,13 @@ struct Tile {
 };
 constexpr int kRing = 16;
 
-// LDS layouts of an operand's 64 K values.  ROW: 128-byte rows, 16-byte chunks
+// LDS layouts of an operand's step.  ROW: 128-byte rows, 16-byte chunks
 // XOR-swizzled.  COL (T): 64 rows of W columns, 32-byte pieces XOR-swizzled.
 __device__ __forceinline__ int swz_row(int row) { return (row >> 1) & 7; }
-__device__ __forceinline__ int swz_col(int krow) { return (krow & 3) | ((krow >> 3) & 1) << 2; }
+template <int W>
+__device__ __forceinline__ int swz_col(int krow) {
+  return ((krow & 3) | ((krow >> 3) & 1) << 2) & (W / 16 < 8 ? W / 16 - 1 : 7);
+}
 
 // Source offset (bytes) of lane `lane` of the wave-load number `ld`.
 template <bool T, int W>
@@ -70,30 +87,22 @@ __device__ __forceinline__ uint32_t load_offset(int ld, int lane, uint32_t pitch
   } else {
     constexpr int CH = W / 8;                       // 16-byte chunks of a K row
     const int krow = ld * (64 / CH) + lane / CH, c = lane % CH;
-    constexpr int MASK = W / 16 < 8 ? W / 16 - 1 : 7;
-    return (uint32_t)krow * pitch + (uint32_t)(((((c >> 1) ^ (swz_col(krow) & MASK)) << 1 | (c & 1)) << 4));
+    return (uint32_t)krow * pitch + (uint32_t)((((c >> 1) ^ swz_col<W>(krow)) << 1 | (c & 1)) << 4);
   }
 }
 
-// Reads of the fragments (16 rows or columns x 32 K values) of a wave: lane (x, q)
-// holds K values 8 q .. + 7 of row or column x.
+// Reads of the fragments (16 rows or columns x 32 K values) of a wave: lane
+// (x, q) holds K values 8 q .. + 7 of half `ks` of the step, of row or column x.
 template <bool T, int W, int F>
 struct Frags {
   static constexpr int N = T ? F : 2;
-  uint32_t off[N];       // ROW: by K half; COL: by fragment
-  uint32_t at[N];        // the same in the stage that is read
+  uint32_t off[N], at[N];       // the lane's offsets in a stage, and in the one that is read; ROW: by half, COL: by fragment
   __device__ __forceinline__ void init(int lane, int wave_base) {
-    const int x = lane & 15, q = lane >> 4;
-    if constexpr (!T) {
+    const int x = lane & 15, q = lane >> 4, krow = 8 * q + (x >> 2);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) off[ks] = (uint32_t)((wave_base + x) * 128 + (((4 * ks + q) ^ swz_row(x)) << 4));
-    } else {
-      constexpr int MASK = W / 16 < 8 ? W / 16 - 1 : 7;
-      const int krow = 8 * q + (x >> 2);
-#pragma unroll
-      for (int i = 0; i < F; ++i)
-        off[i] = (uint32_t)(krow * 2 * W + (((wave_base / 16 + i) ^ (swz_col(krow) & MASK)) << 5) + 8 * (x & 3));
-    }
+    for (int i = 0; i < N; ++i)
+      off[i] = !T ? (uint32_t)((wave_base + x) * 128 + (((4 * i + q) ^ swz_row(x)) << 4))
+                  : (uint32_t)(krow * 2 * W + (((wave_base / 16 + i) ^ swz_col<W>(krow)) << 5) + 8 * (x & 3));
   }
   __device__ __forceinline__ void stage(uint32_t base, int ks) {
 #pragma unroll
@@ -166,7 +175,8 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(Half
   // bytes (the others).
   int lround = 0, lk = 0, kleft = 0;
   const uint8_t *pa = nullptr, *pb = nullptr;
-  uint32_t la = 0, lb = 0, ca = 0, cb = 0, live = 0;
+  int la = 0, lb = 0;
+  uint32_t ca = 0, cb = 0;
   const uint32_t pitch_a = (uint32_t)(AT ? p.rows : p.k) * 2, pitch_b = (uint32_t)(BT ? p.n : p.k) * 2;
 
   // Tiles are numbered in blocks of 8 m-tiles x all n-tiles, n-major inside a
@@ -175,7 +185,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(Half
   auto plan = [&](int round) {
     int id = tile_at(round);
     Tile t{0, 0x7FFFFFFF, 0, 0, 0};
-    la = lb = live = 0;
+    la = lb = 0;
     kleft = 0;
     pa = pb = reinterpret_cast<const uint8_t*>(p.a);
     if (id < total) {
@@ -214,12 +224,11 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(Half
         t.nk = (int)((p.k + 63) / 64);
         const int64_t mm = t.row_end - t.row0 < C::BM ? t.row_end - t.row0 : C::BM;
         pa = reinterpret_cast<const uint8_t*>(p.a + t.row0 * p.k);
-        la = ufirst((uint32_t)(mm * p.k * 2));
+        la = (int)ufirst((uint32_t)(mm * p.k * 2));
         pb = reinterpret_cast<const uint8_t*>(p.b + t.g * p.n * p.k + t.n0 * (BT ? 1 : p.k));
-        lb = ufirst((uint32_t)(nn * p.k * 2));
+        lb = (int)ufirst((uint32_t)(nn * p.k * 2));
         kleft = (int)p.k;
         cb = (uint32_t)t.n0 * 2;
-        live = 128;
       }
     }
     lk = t.nk;
@@ -234,25 +243,24 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(Half
   for (int i = 0; i < AL; ++i) va[i] = load_offset<AT, C::BM>(i * C::WAVES + w, lane, pitch_a);
 #pragma unroll
   for (int i = 0; i < BL; ++i) vb[i] = load_offset<BT, C::BN>(i * C::WAVES + w, lane, pitch_b);
-  // row operands: bit 31 drops the chunks past K of its last step (the swizzle does not depend on i)
-  const uint32_t krem = (uint32_t)p.k & 63;
-  const uint32_t drop = !AT && krem != 0 && (uint32_t)(((lane & 7) ^ swz_row(w * 8 + (lane >> 3))) * 8) >= krem ? 0x80000000u : 0u;
+  // row operands: the first K value of the lane's chunk (the swizzle does not
+  // depend on i); bit 31 of an offset drops a chunk that lies past K
+  const int chunk = ((lane & 7) ^ swz_row(w * 8 + (lane >> 3))) * 8;
+  auto past_k = [&]() -> uint32_t { return AT || chunk < kleft ? 0u : 0x80000000u; };
   constexpr int kOps = AL + BL;
   // bytes of a step that may be read, from its first one
-  auto limit = [&](bool t, uint32_t bytes, uint32_t pitch, uint32_t c) -> uint32_t {
-    if (!t) return bytes;
+  auto limit = [&](bool t, int bytes, uint32_t pitch, uint32_t c) -> uint32_t {
+    if (!t) return (uint32_t)bytes;
     return kleft <= 0 ? 0u : (uint32_t)(kleft < 64 ? kleft : 64) * pitch - c;
   };
-  // load l (B's, then A's) of the cursor's step into the stage at stage_at
-  auto issue1 = [&](int l, uint32_t stage_at) {
-    const uint32_t mask = !AT && lk == 1 ? drop : 0u;
-    if (l < BL) {
-      const uint32_t v = BT ? vb[l] : vb[l] | mask;
-      dma16(rsrc(pb, limit(BT, lb, pitch_b, cb)), v, 0, stage_at + C::BM * 128 + (uint32_t)(l * C::WAVES + w) * 1024);
-    } else {
-      const uint32_t v = AT ? va[l - BL] : va[l - BL] | mask;
-      dma16(rsrc(pa, limit(AT, la, pitch_a, ca)), v, 0, stage_at + (uint32_t)((l - BL) * C::WAVES + w) * 1024);
-    }
+  auto source_a = [&]() { return rsrc(pa, limit(AT, la, pitch_a, ca)); };
+  auto source_b = [&]() { return rsrc(pb, limit(BT, lb, pitch_b, cb)); };
+  // load l of an operand's step into the stage at stage_at
+  auto load_a = [&](int l, const __amdgpu_buffer_rsrc_t& r, uint32_t stage_at, uint32_t past) {
+    dma16(r, AT ? va[l] : va[l] | past, 0, stage_at + (uint32_t)(l * C::WAVES + w) * 1024);
+  };
+  auto load_b = [&](int l, const __amdgpu_buffer_rsrc_t& r, uint32_t stage_at, uint32_t past) {
+    dma16(r, BT ? vb[l] : vb[l] | past, 0, stage_at + C::BM * 128 + (uint32_t)(l * C::WAVES + w) * 1024);
   };
   auto advance = [&]() {
     if (--lk == 0) {
@@ -260,14 +268,18 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(Half
     } else {
       pa += AT ? (int64_t)pitch_a * 64 : 128;
       pb += BT ? (int64_t)pitch_b * 64 : 128;
-      la -= live;
-      lb -= live;
+      la = la - 128 > 0 ? la - 128 : 0;           // signed: a scalar maximum
+      lb = lb - 128 > 0 ? lb - 128 : 0;
       kleft -= 64;
     }
   };
   for (int s = 0; s < ST; ++s) {
+    const __amdgpu_buffer_rsrc_t rb0 = source_b(), ra0 = source_a();
+    const uint32_t past = past_k();
 #pragma unroll
-    for (int l = 0; l < kOps; ++l) issue1(l, lds0 + (uint32_t)s * C::STAGE);
+    for (int l = 0; l < BL; ++l) load_b(l, rb0, lds0 + (uint32_t)s * C::STAGE, past);
+#pragma unroll
+    for (int l = 0; l < AL; ++l) load_a(l, ra0, lds0 + (uint32_t)s * C::STAGE, past);
     advance();
   }
 
@@ -281,39 +293,52 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(Half
   uint32_t stage = lds0;                 // of the current step
   auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
   auto next_stage = [&]() { return stage + C::STAGE == lds0 + ST * C::STAGE ? lds0 : stage + C::STAGE; };
-  // read number r of the set `set` (B's, then A's), after read_from
-  auto read_from = [&](int set, uint32_t at) {
-    fb.stage(at + C::BM * 128, set);
-    fa.stage(at, set);
+  // read number r of half ks of a step (B's, then A's), after read_from
+  auto read_from = [&](int ks, uint32_t at) {
+    fb.stage(at + C::BM * 128, ks);
+    fa.stage(at, ks);
   };
-  auto read1 = [&](int r, int set) {
-    if (r < FJ) rb[set][r] = fb.read(r, set);
-    else ra[set][r - FJ] = fa.read(r - FJ, set);
+  auto read1 = [&](int r, int ks) {
+    if (r < FJ) rb[ks][r] = fb.read(r, ks);
+    else ra[ks][r - FJ] = fa.read(r - FJ, ks);
   };
   constexpr int R = FI + FJ, G = FI * FJ;
-  // the products of one set, with the reads of the other set (from `at`) and, for
-  // set 1, the loads into the freed stage spread over them
-  auto sub = [&](auto setc, uint32_t at, uint32_t freed) {
-    constexpr int set = decltype(setc)::value;
-    read_from(set ^ 1, at);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int i = g / FJ, j = g % FJ;
-      mfma<F16, C::AGPR>(acc[i][j], rb[set][j], ra[set][i]);
-#pragma unroll
-      for (int r = g * R / G; r < (g + 1) * R / G; ++r) read1(r, set ^ 1);
-      if constexpr (set == 1) {
-#pragma unroll
-        for (int l = g * kOps / G; l < (g + 1) * kOps / G; ++l) issue1(l, freed);
+  // A step's halves.  The products of half ks, with the reads of the next half
+  // (of the stage at `at`) among them.  In the first half all of B has been read
+  // when its fragments for the second are in registers: a barrier then frees its
+  // part of the stage, and the loads of the step ST later go there; the second half
+  // starts with the barrier that frees A's part, and has A's loads.  So the
+  // loads are spread over the step, as the address unit needs them: bunched in
+  // its second half they held the matrix instructions up.
+  constexpr int kFreeB = G / 4;
+  auto half = [&](auto ksc, uint32_t at, uint32_t freed) {
+    constexpr int ks = decltype(ksc)::value;
+    read_from(ks ^ 1, at);
+    const uint32_t past = past_k();
+    const __amdgpu_buffer_rsrc_t src = ks == 0 ? source_b() : source_a();
+    each<G>([&](auto gc) {
+      constexpr int g = decltype(gc)::value, i = g / FJ, j = g % FJ;
+      if constexpr (ks == 0 && g == kFreeB) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        bar();
+      }
+      mfma<F16, C::BIG>(acc[i][j], rb[ks][j], ra[ks][i]);
+      if constexpr (ks == 0) {
+        each<FJ>([&](auto r) { if constexpr (r.value * kFreeB / 2 / FJ == g) read1(r.value, 1); });
+        each<FI>([&](auto r) { if constexpr (kFreeB + r.value * (G / 2) / FI == g) read1(FJ + r.value, 1); });
+        each<BL>([&](auto l) { if constexpr (kFreeB + l.value * (G - kFreeB) / BL == g) load_b(l.value, src, freed, past); });
+      } else {
+        each<R>([&](auto r) { if constexpr (r.value * (G / 2) / R == g) read1(r.value, 0); });
+        each<AL>([&](auto l) { if constexpr (l.value * G / AL == g) load_a(l.value, src, freed, past); });
       }
       fence();
-    }
+    });
   };
 
   // Wait states between matrix instructions and vector instructions that write
   // or read their sums: 19 cover the longest need of a 16 x 16 x 32 product.
   auto keep = [](v4f& v) {
-    if constexpr (C::AGPR) asm volatile("" : "+a"(v));
+    if constexpr (C::BIG) asm volatile("" : "+a"(v));
     else asm volatile("" : "+v"(v));
   };
   auto keep_all = [&]() {
@@ -352,14 +377,14 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(Half
       for (int j = 0; j < FJ; ++j) acc[i][j] = v4f{};
     settle();
     for (int k = 0; k < t.nk; ++k) {
-      sub(std::integral_constant<int, 0>(), stage, 0);
-      // the stage has been read by this wave; the next step's has landed
+      half(std::integral_constant<int, 0>(), stage, stage);
+      // this wave has read its stage, and the next step's has landed
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      wait_vm<(ST - 2) * kOps>();
+      wait_vm<(ST - 2) * kOps + BL>();
       bar();
       const uint32_t freed = stage;
       stage = next_stage();
-      sub(std::integral_constant<int, 1>(), stage, freed);
+      half(std::integral_constant<int, 1>(), stage, freed);
       advance();
     }
     settle();
