@@ -127,7 +127,7 @@ struct Frags {
 
 // AT / BT: the operand lies K-major outside (K rows of columns).
 template <class C, bool AT, bool BT, bool F16>
-__global__ __launch_bounds__(C::THREADS, C::WAVES / 4) void half_gemm_tiled(HalfGemmArgs p) {
+__global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p) {
   constexpr int FI = C::FI, FJ = C::FJ, ST = C::ST, AL = C::AL, BL = C::BL;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ Table table;
