@@ -1,7 +1,7 @@
 """CPU test of the built library's code: the 16-bit products' matrix instructions are
 written as inline assembly, around which the compiler adds none of the wait
 states that gfx950 needs between vector and matrix instructions.  Disassembled,
-in every kernel of theirs
+in every tiled kernel of theirs
   - a vector instruction that writes an operand of a matrix instruction comes two
     wait states before it at least;
   - an instruction other than a matrix one that reads or writes a matrix
@@ -98,7 +98,7 @@ def test_products_wait(tmp_path):
     for f in sorted(tmp_path.glob("lib.so.*gfx950")):
         out = subprocess.run([tool, "-d", "--no-show-raw-insn", str(f)], check=True, capture_output=True, text=True).stdout
         for part in re.split(r"\n(?=[0-9a-f]+ <[^>]*>:\n)", out):
-            if "half_gemm" not in part.split("\n", 1)[0]:
+            if "half_gemm_tiled" not in part.split("\n", 1)[0]:
                 continue
             n, b = _violations(part.splitlines()[1:])
             count += n
