@@ -17,6 +17,7 @@ using hq::api::ok;
 
 namespace {
 
+constexpr int64_t kMaxPlaces = (int64_t)1 << 30;     // places and tokens of an adapters' batch
 constexpr int64_t kMaxWidth = (int64_t)1 << 21;      // 256 rows of it stay below 2^31 bytes
 
 hq_status check_groups(const char* what, int32_t num_groups) {
@@ -93,18 +94,17 @@ hq_status check_lora_shape(const char* what, int64_t max_rows, int64_t n, int64_
   if ((st = check_width(what, "k", k, 8)) != HQ_OK) return st;
   if (r < 8 || r % 8 != 0 || r > 512)
     return fail(HQ_ERR_SHAPE, "%s: r=%lld must be a multiple of 8 in [8, 512]", what, (long long)r);
-  if (max_rows < 0 || max_rows > kI32)
-    return fail(HQ_ERR_SHAPE, "%s: max_rows=%lld must be in [0, 2^31)", what, (long long)max_rows);
-  const int64_t wide = n > k ? n : k;
-  if ((max_rows / 16 + adapters + 1) * (wide / 16 + 1) > kI32)
-    return fail(HQ_ERR_SHAPE, "%s: problem too large (tile count exceeds 2^31)", what);
+  if (max_rows < 0 || max_rows >= kMaxPlaces)
+    return fail(HQ_ERR_SHAPE, "%s: max_rows=%lld must be in [0, 2^30)", what, (long long)max_rows);
   return HQ_OK;
 }
 
 // Checks common to both directions, after the shape's.
 hq_status check_lora(const char* what, const hq::LoraArgs& p, uint64_t need, uint64_t workspace_bytes) {
   const hq::LoraPlan& pl = p.plan;
-  if (pl.m < 0 || pl.m > kI32) return fail(HQ_ERR_SHAPE, "%s: m=%lld must be in [0, 2^31)", what, (long long)pl.m);
+  if (pl.m < 0 || pl.m >= kMaxPlaces) return fail(HQ_ERR_SHAPE, "%s: m=%lld must be in [0, 2^30)", what, (long long)pl.m);
+  if (hq::lora_work_items(pl.max_rows, pl.m, p.n, p.k, p.r, pl.adapters) >= hq::kMaxWorkItems)
+    return fail(HQ_ERR_SHAPE, "%s: problem too large (a launch would pass 2^32 work items)", what);
   if ((pl.row_map != nullptr) != (pl.row_pair != nullptr) && pl.m > 0 && pl.max_rows > 0)
     return fail(HQ_ERR_NULL, "%s: row_map and row_pair go together", what);
   if (pl.row_pair == nullptr && pl.max_rows != pl.m)
@@ -304,6 +304,7 @@ hq_status hq_lora_backward(void* stream, uint32_t flags, const uint16_t* dy, con
   if (base != nullptr && dx == nullptr) return fail(HQ_ERR_NULL, "%s: base needs dx", what);
   if (!da || !db || (m > 0 && (!dy || !x || !a || !b)) || (m > 0 && max_rows > 0 && !v))
     return fail(HQ_ERR_NULL, "%s: dy, x, v, a, b, da and db are required", what);
+  if (m == 0) p.plan.max_rows = 0;          // no place holds a token: the sums are empty
   hq::DeviceInfo dev;
   if ((st = current_device(&dev)) != HQ_OK) return st;
   return launched(hq::launch_lora_backward((hipStream_t)stream, p), what);

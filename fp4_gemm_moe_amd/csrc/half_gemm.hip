@@ -1,90 +1,22 @@
 // 16-bit products by expert: out[r] = a[r] b[g]^T (or a[r] b[g]) for the rows r
 // of group g, and out[g] = sum over its rows of a[r]^T b[r].  The direct kernel
 // for calls of few rows, and the choice of kernel and tile.
+#include "group_tiles.hpp"
 #include "half_launch.hpp"
+#include "half_math.hpp"
 
 namespace hq {
 namespace {
 
-typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-
-template <bool F16>
-__device__ __forceinline__ v4f product16(v4i w, v4i x, v4f c) {
-  if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, x), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, w), __builtin_bit_cast(v8b, x), c, 0, 0, 0);
-}
-
-// The group and rows of m-tile `mt` (16 rows) of the groups, found by each wave
-// on its own: a lane has a run of at most 16 groups.  g < 0: there is no such tile.
-struct DirectTile {
-  int g, row0, row_end;
-};
-__device__ __forceinline__ DirectTile direct_tile(const HalfGemmArgs& p, int mt) {
-  const int lane = threadIdx.x & 63, per = (p.groups + 63) / 64;
-  const bool masked = p.form == kMasked;
-  int top = 0, tiles = 0;
-  // the largest end of the lane's run, and of those before it (clamped ends never decrease)
-  if (!masked) {
-    for (int i = 0; i < per; ++i) {
-      const int g = lane * per + i, e = g < p.groups ? p.group_end[g] : 0;
-      top = e > top ? e : top;
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int v = __shfl_up(top, off, 64);
-      if (lane >= off && v > top) top = v;
-    }
-    top = __shfl_up(top, 1, 64);
-    if (lane == 0) top = 0;
-  }
-  const int rows = (int)p.rows;
-  auto span = [&](int g, int& prev, int& start, int& end) {       // rows of group g; prev: the end before it
-    if (masked) {
-      const int64_t v = p.counts[g], c = v < 0 ? 0 : (v > p.slot_rows ? p.slot_rows : v);
-      start = (int)(g * p.slot_rows);
-      end = start + (int)c;
-    } else {
-      const int e = p.group_end[g];
-      start = prev < rows ? prev : rows;
-      prev = e > prev ? e : prev;
-      end = prev < rows ? prev : rows;
-    }
-  };
-  int prev = top, start, end;
-  for (int i = 0; i < per; ++i) {
-    const int g = lane * per + i;
-    if (g >= p.groups) break;
-    span(g, prev, start, end);
-    tiles += (end - start + 15) / 16;
-  }
-  int upto = tiles;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int v = __shfl_up(upto, off, 64);
-    if (lane >= off) upto += v;
-  }
-  const int owner = __popcll(__ballot(upto <= mt));
-  if (owner >= 64) return {-1, 0, 0};
-  DirectTile t{-1, 0, 0};
-  if (lane == owner) {
-    int left = mt - (upto - tiles);
-    prev = top;
-    for (int i = 0; i < per; ++i) {
-      const int g = lane * per + i;
-      span(g, prev, start, end);
-      const int n = (end - start + 15) / 16;
-      if (left < n) {
-        t = {g, start + left * 16, end};
-        break;
-      }
-      left -= n;
-    }
-  }
-  t.g = __builtin_amdgcn_readlane(t.g, owner);
-  t.row0 = __builtin_amdgcn_readlane(t.row0, owner);
-  t.row_end = __builtin_amdgcn_readlane(t.row_end, owner);
+// The group and rows of m-tile `mt` (16 rows); g < 0: there is no such tile.
+__device__ __forceinline__ GroupTile direct_tile(const HalfGemmArgs& p, int mt) {
+  if (p.form == kContiguous) return group_tile(p.group_end, p.groups, (int)p.rows, 16, mt);
+  const int per = (int)((p.slot_rows + 15) / 16), g = mt / per;
+  const int64_t v = p.counts[g], c = v < 0 ? 0 : (v > p.slot_rows ? p.slot_rows : v);
+  GroupTile t{};
+  t.row0 = (int)(g * p.slot_rows) + (mt - g * per) * 16;
+  t.row_end = (int)(g * p.slot_rows + c);
+  t.g = t.row0 < t.row_end ? g : -1;
   return t;
 }
 
@@ -98,7 +30,7 @@ __device__ __forceinline__ DirectTile direct_tile(const HalfGemmArgs& p, int mt)
 template <bool F16, int W, int U>
 __global__ __launch_bounds__(W * 64) void half_gemm_direct(HalfGemmArgs p) {
   __shared__ v4f part[W - 1][64];
-  const DirectTile t = direct_tile(p, blockIdx.y);
+  const GroupTile t = direct_tile(p, blockIdx.y);
   if (t.g < 0) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int x = lane & 15, q = lane >> 4, k = (int)p.k;

@@ -6,14 +6,13 @@
 
 #include "block_gemm.hpp"
 #include "half_internal.hpp"
+#include "half_math.hpp"
 #include "tile_util.hpp"
 
 namespace hq {
 namespace half {
 
 using namespace blk;
-
-typedef short v4s __attribute__((ext_vector_type(4)));
 
 // acc += a b^T for fragments of 16 x 32 values (BF16 or FP16 bits), in place: as
 // builtins the compiler gives results other registers than the sums they

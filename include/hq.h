@@ -730,7 +730,8 @@ hq_status hq_swiglu_backward(void* stream, const uint16_t* dy, const uint16_t* x
  *   v  [max_rows, r] FP32 (NULL: not kept): x A^T by place, which the gradients
  *      need; places without a token are not written.
  * r % 8 == 0, 8 <= r <= 512; n % 8 == 0, k % 8 == 0, both below 2^21 and
- * positive; max_rows < 2^31; 1 <= num_adapters <= 1024.  The workspace holds
+ * positive; m and max_rows below 2^30; 1 <= num_adapters <= 1024; a launch's work
+ * items below 2^32 (HQ_ERR_SHAPE otherwise).  The workspace holds
  * hq_lora_workspace_size bytes; two calls in flight need two.  16-bit tensors,
  * v, da, db and the workspace are 16-byte aligned, the others 4-byte.  m == 0
  * writes nothing but, in the gradient, da and db.

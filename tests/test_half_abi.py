@@ -98,7 +98,8 @@ def test_swiglu_backward_refuses(lib, kw, code):
 
 LORA = [(dict(n=12), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(k=1 << 21), SHAPE), (dict(r=0), SHAPE),
         (dict(r=12), SHAPE), (dict(r=520), SHAPE), (dict(L=0), SHAPE), (dict(L=1025), SHAPE), (dict(m=-1), SHAPE),
-        (dict(rows=-1), SHAPE), (dict(rows=1 << 31), SHAPE), (dict(rows=(1 << 31) - 1, n=1 << 20), SHAPE),
+        (dict(rows=-1), SHAPE), (dict(rows=1 << 30), SHAPE), (dict(m=1 << 30), SHAPE),
+        (dict(rows=(1 << 30) - 1, n=1 << 20, k=1 << 20), SHAPE),
         (dict(map=NUL, pair=NUL, rows=65), SHAPE), (dict(wsb=0), SHAPE), (dict(map=NUL), NULL), (dict(pair=NUL), NULL),
         (dict(ends=NUL), NULL), (dict(ws=NUL), NULL), (dict(x=NUL), NULL), (dict(a=NUL), NULL), (dict(b=NUL), NULL),
         (dict(x=FOUR), ALIGN), (dict(a=MIS), ALIGN), (dict(b=FOUR), ALIGN), (dict(base=FOUR), ALIGN),
