@@ -11,27 +11,28 @@ struct GroupTile {
   int g;                 // the group; -1: there is none
   int row0, row_end;     // the tile's first row, the group's end
   int index, first;      // the tile's number among all, and that of its group's first one
-  int last;              // the last group's end
 };
 
-// Inclusive scans over a wave's lanes.
-__device__ __forceinline__ int wave_scan_add(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(v, off, 64);
-    if (lane >= off) v += o;
-  }
-  return v;
+// Inclusive scans over a wave's lanes of non-negative values, by DPP moves: within
+// rows of 16 lanes, then each row's last lane into the rows behind it.
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));      // row_shr:1
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));      // row_shr:2
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));      // row_shr:4
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));      // row_shr:8
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));      // row_bcast:15, rows 1 and 3
+  return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));   // row_bcast:31, rows 2 and 3
 }
-__device__ __forceinline__ int wave_scan_max(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(v, off, 64);
-    if (lane >= off && o > v) v = o;
-  }
-  return v;
+// The value of the lane before, 0 in the first.
+__device__ __forceinline__ int lane_before(int v) { return __builtin_amdgcn_update_dpp(0, v, 0x138, 0xf, 0xf, false); }
+
+// The last group's end.
+__device__ __forceinline__ int last_end(const int32_t* __restrict__ ends, int groups, int rows) {
+  int top = 0;
+  for (int g = threadIdx.x & 63; g < groups; g += 64) top = ends[g] > top ? ends[g] : top;
+  top = __builtin_amdgcn_readlane(wave_scan(top, OpMax()), 63);
+  return top < rows ? top : rows;
 }
 
 // Tile number `want` of bm rows (by_group: the first tile of group `want`, with
@@ -45,10 +46,7 @@ __device__ __forceinline__ GroupTile group_tile(const int32_t* __restrict__ ends
     const int g = lane * per + i, e = g < groups ? ends[g] : 0;
     top = e > top ? e : top;
   }
-  const int upto_end = wave_scan_max(top);
-  const int last_raw = __shfl(upto_end, 63, 64), last = last_raw < rows ? last_raw : rows;
-  int before = __shfl_up(upto_end, 1, 64);
-  if (lane == 0) before = 0;
+  const int upto_end = wave_scan(top, OpMax()), before = lane_before(upto_end);
   // the run's groups: start and end of each from the largest end so far
   auto walk = [&](auto f) {
     int prev = before;
@@ -63,9 +61,9 @@ __device__ __forceinline__ GroupTile group_tile(const int32_t* __restrict__ ends
   };
   int tiles = 0;
   walk([&](int, int, int, int n) { tiles += n; return false; });
-  const int upto = wave_scan_add(tiles);
+  const int upto = wave_scan(tiles, OpAdd());
   const int owner = by_group ? want / per : __popcll(__ballot(upto <= want));
-  GroupTile t{-1, 0, 0, want, 0, last};
+  GroupTile t{-1, 0, 0, want, 0};
   if (owner >= 64) return t;
   int index = upto - tiles;
   if (lane == owner)

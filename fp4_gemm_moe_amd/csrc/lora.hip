@@ -22,10 +22,11 @@ __device__ __forceinline__ v4i load8(const uint16_t* p) { return *reinterpret_ca
 // ------------------------------------------------------------------ shrink
 constexpr int kShrinkWaves = 8;
 
-// Partial sums of a workgroup: 16 MF places x 16 RF ranks over one slice of K.
-// Its waves take blocks of 64 K values in turn, each lane loading its operands
-// from memory (w [K, r]: through the wave's share of LDS, read transposed), and
-// their sums meet in LDS in the order of the waves.
+// Partial sums of a workgroup: 16 MF RW places x 16 RF ranks over one slice of K.
+// Its waves are RW groups of places times W / RW that take blocks of 64 K values in
+// turn, each lane loading its operands from memory (w [K, r]: through the wave's
+// share of LDS, read transposed); waves of the same block share w's lines in
+// the first-level cache.  Their sums meet in LDS in the order of the waves.
 struct ShrinkArgs {
   LoraPlan pl;
   const uint16_t* z;       // [m, k]
@@ -34,9 +35,9 @@ struct ShrinkArgs {
   int k, r, slices;
 };
 
-template <bool F16, bool WT, int MF, int RF>
+template <bool F16, bool WT, int RW, int MF, int RF>
 __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
-  constexpr int W = kShrinkWaves, RN = 16 * RF, PITCH = RN * 2 + 16;
+  constexpr int W = kShrinkWaves, KW = W / RW, RN = 16 * RF, PITCH = RN * 2 + 16;
   constexpr int U = WT ? 1 : 2;                     // blocks in flight
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), x = lane & 15, q = lane >> 4;
   const int chunks = (p.r + RN - 1) / RN;
@@ -44,13 +45,14 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
   const int slice = id % p.slices;
   id /= p.slices;
   const int r0 = id % chunks * RN;
-  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 16 * MF, id / chunks);
+  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 16 * MF * RW, id / chunks);
   if (t.g < 0) return;
+  const int wk = w / RW, place0 = t.row0 + w % RW * 16 * MF;
   const uint16_t* zp[MF];
   bool live[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    const int place = t.row0 + 16 * i + x;
+    const int place = place0 + 16 * i + x;
     const int64_t tok = place < t.row_end ? token_at(p.pl, place) : -1;
     live[i] = tok >= 0;
     zp[i] = p.z + (tok >= 0 ? tok : 0) * p.k + 8 * q;
@@ -71,7 +73,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
 #pragma unroll
     for (int j = 0; j < RF; ++j) acc[i][j] = v4f{0, 0, 0, 0};
   const int blocks = (p.k + 63) / 64, last = blocks * (slice + 1) / p.slices;
-  for (int b = blocks * slice / p.slices + w * U; b < last; b += W * U) {
+  for (int b = blocks * slice / p.slices + wk * U; b < last; b += KW * U) {
     v4i zf[U][2][MF], wf[U][2][RF];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -134,14 +136,29 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
 #pragma unroll
     for (int j = 0; j < RF; ++j) part[(w * MF * RF + i * RF + j) * 64 + lane] = acc[i][j];
   __syncthreads();
-  for (int f = w; f < MF * RF; f += W) {
-    v4f s = part[f * 64 + lane];
+  for (int f = wk; f < MF * RF; f += KW) {
+    v4f s = part[(w % RW * MF * RF + f) * 64 + lane];
 #pragma unroll
-    for (int e = 1; e < W; ++e) s += part[(e * MF * RF + f) * 64 + lane];
-    const int i = f / RF, place = t.row0 + 16 * i + x, rank = r0 + 16 * (f % RF) + 4 * q;
+    for (int e = 1; e < KW; ++e) s += part[((e * RW + w % RW) * MF * RF + f) * 64 + lane];
+    const int place = place0 + 16 * (f / RF) + x, rank = r0 + 16 * (f % RF) + 4 * q;
     if (place < t.row_end && rank < p.r && token_at(p.pl, place) >= 0)
       *reinterpret_cast<v4f*>(p.out + ((int64_t)slice * p.pl.max_rows + place) * p.r + rank) = s;
   }
+}
+
+// The sum of the slices' partial sums, in order, for every place with a token.
+__global__ __launch_bounds__(256) void lora_slices(LoraPlan pl, const float* part, int r, int slices, float* out) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = pl.max_rows * r;
+  if (at >= all || token_at(pl, (int)(at / r)) < 0) return;
+  v4f v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (e < slices) v[e] = *reinterpret_cast<const v4f*>(part + e * all + at);
+  v4f s = v[0];
+#pragma unroll
+  for (int e = 1; e < 16; ++e)
+    if (e < slices) s += v[e];
+  *reinterpret_cast<v4f*>(out + at) = s;
 }
 
 // ------------------------------------------------------------------ expand
@@ -155,207 +172,343 @@ struct ExpandArgs {
   uint16_t* out;           // [m, n]
   float* v_out;            // the slices' sums (nullptr: not kept)
   int n, r, slices;
-  int chunk;               // columns of a workgroup, a multiple of 256
-  int chunks;
+  int chunk, chunks;       // columns of a workgroup, a multiple of 256
   unsigned tiles, rest;    // workgroups of places, of tokens without an adapter
+  int rest_chunks;
 };
-constexpr int kRestRows = 64;
-constexpr int kWtRanks = 64;             // WT: ranks of w in LDS at a time
+constexpr int kRestRows = 64, kRestCols = 2048;
 
-// Bytes of LDS: 16 MF places of r values as two 16-bit parts, and their factors; WT:
-// a wave's 64 columns of w.
-template <bool WT, int MF>
-constexpr int expand_smem(int r) {
-  return 16 * MF * ((r + 15) / 16 * 64 + 16) + 16 * MF * 4 + (WT ? 4 * kWtRanks * 144 : 0);
-}
-
-// Tokens without an adapter: base's row, or zeros.
+// Tokens without an adapter: base's row, or zeros.  A workgroup: 64 tokens, whose
+// places its waves look up a lane each, and a share of the columns.
 __device__ __forceinline__ void expand_rest(const ExpandArgs& p, int id) {
-  const int c0 = id % p.chunks * p.chunk, c1 = c0 + p.chunk < p.n ? c0 + p.chunk : p.n;
-  const int64_t t0 = (int64_t)(id / p.chunks) * kRestRows;
-  const int last = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 1, 0).last;
+  const int c0 = id % p.rest_chunks * kRestCols;
+  const int64_t t0 = (int64_t)(id / p.rest_chunks) * kRestRows;
+  const int last = last_end(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int i = wave; i < kRestRows; i += 4) {
-    const int64_t t = t0 + i;
-    if (t >= p.pl.m) break;
-    const int64_t place = p.pl.row_map != nullptr ? p.pl.row_map[t] : t;
-    if (place >= 0 && place < last) continue;
-    for (int c = c0 + lane * 8; c < c1; c += 512)
-      *reinterpret_cast<v4i*>(p.out + t * p.n + c) = p.base != nullptr ? load8(p.base + t * p.n + c) : v4i{0, 0, 0, 0};
+  bool none = false;
+  if (t0 + lane < p.pl.m) {
+    const int64_t place = p.pl.row_map != nullptr ? p.pl.row_map[t0 + lane] : t0 + lane;
+    none = place < 0 || place >= last;
+  }
+  uint64_t left = __ballot(none);
+  for (int i = 0; left != 0; ++i, left &= left - 1) {
+    if ((i & 3) != wave) continue;
+    const int64_t at = (t0 + __builtin_ctzll(left)) * p.n;
+    v4i v[kRestCols / 512];
+#pragma unroll
+    for (int e = 0; e < kRestCols / 512; ++e) {
+      v[e] = v4i{0, 0, 0, 0};
+      if (p.base != nullptr && c0 + lane * 8 + 512 * e < p.n) v[e] = load8(p.base + at + c0 + lane * 8 + 512 * e);
+    }
+#pragma unroll
+    for (int e = 0; e < kRestCols / 512; ++e)
+      if (c0 + lane * 8 + 512 * e < p.n) *reinterpret_cast<v4i*>(p.out + at + c0 + lane * 8 + 512 * e) = v[e];
   }
 }
 
-// A workgroup: 16 MF places, `chunk` columns; each wave 64 of every 256.  A place's
-// value v scale is kept as hi + lo: 16 ranks' hi and 16 ranks' lo are the 32 K
-// values of one matrix product with the ranks' weights twice.  BF16: hi the value
-// cut to 8 bits, lo the rest rounded.  FP16: the place's values are first scaled
-// by the power of two that takes the largest to [2^14, 2^15), undone in FP32 at
-// the end, so that neither part leaves FP16's range.
-template <bool F16, bool WT, int MF>
-__device__ __forceinline__ void expand_tile(const ExpandArgs& p, int id) {
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), x = lane & 15, q = lane >> 4;
-  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 16 * MF, id / p.chunks);
-  if (t.g < 0) return;
-  const int chunk_no = id % p.chunks, c0 = chunk_no * p.chunk, c1 = c0 + p.chunk < p.n ? c0 + p.chunk : p.n;
-  const int steps = (p.r + 15) / 16, pitch = steps * 64 + 16;
-  uint8_t* vt = smem;
-  float* fac = reinterpret_cast<float*>(smem + 16 * MF * pitch);
-  uint8_t* wt = smem + 16 * MF * (pitch + 4) + w * kWtRanks * 144;
-  const float scale = p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
+// The values v scale of a wave's 16 places as fragments: each is kept as hi + lo, and
+// 16 ranks' hi and 16 ranks' lo are the 32 K values of a matrix product with
+// the ranks' weights twice (lanes q < 2: hi, the others: lo, of ranks 16 s + 8 (q % 2)
+// .. + 7).  BF16: hi is the value cut to 8 bits, lo the rest rounded.  FP16: a
+// place's values are first scaled by the power of two that takes its largest to
+// [2^14, 2^15), undone in FP32 at the end, so that neither part leaves FP16's range.
+template <bool F16, int STEPS>
+struct Places {
+  v4i part[STEPS];
+  float factor, back;      // the place's power of two, and the one that undoes it
+  int place;
+  int64_t tok;             // -1: none
 
-  // the places' values: 16 threads a place, in pairs of ranks
-#pragma unroll 1
-  for (int i = tid >> 4; i < 16 * MF; i += 16) {
-    const int place = t.row0 + i;
-    const bool on = place < t.row_end && token_at(p.pl, place) >= 0;
-    auto value = [&](int rank) -> float2 {
-      float2 s = make_float2(0.0f, 0.0f);
-      if (!on || rank >= p.r) return s;
-      const float* src = p.v + (int64_t)place * p.r + rank;
-      s = *reinterpret_cast<const float2*>(src);
-      for (int e = 1; e < p.slices; ++e) {
-        const float2 o = *reinterpret_cast<const float2*>(src + (int64_t)e * p.pl.max_rows * p.r);
-        s.x += o.x;
-        s.y += o.y;
-      }
-      return s;
-    };
-    float f = 1.0f, back = 1.0f;
-    if constexpr (F16) {
-      uint32_t top = 0;
-      for (int rank = 2 * x; rank < p.r; rank += 32) {
-        const float2 s = value(rank);
-        const uint32_t a = __float_as_uint(s.x * scale) & 0x7fffffffu, b = __float_as_uint(s.y * scale) & 0x7fffffffu;
-        top = a > top ? a : top;
-        top = b > top ? b : top;
-      }
-#pragma unroll
-      for (int off = 1; off < 16; off <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)top, off, 16);
-        top = o > top ? o : top;
-      }
-      int e = (int)(top >> 23);                                        // biased exponent
-      e = e < 15 ? 15 : (e > 254 ? 141 : e);                           // Inf and NaN: unscaled
-      f = __uint_as_float((uint32_t)(127 + 141 - e) << 23);
-      back = __uint_as_float((uint32_t)(127 - 141 + e) << 23);
-    }
-    for (int rank = 2 * x; rank < steps * 16; rank += 32) {
-      const float2 s = value(rank);
-      if (p.v_out != nullptr && chunk_no == 0 && on && rank < p.r)
-        *reinterpret_cast<float2*>(p.v_out + (int64_t)place * p.r + rank) = s;
-      const float a = s.x * scale, b = s.y * scale;
-      uint32_t hi, lo;
-      if constexpr (F16) {
-        const float fa = a * f, fb = b * f;
-        hi = pack_half2<true>(fa, fb);
-        const float ha = f16_lo(hi), hb = f16_hi(hi);
-        lo = pack_half2<true>(__builtin_fabsf(ha) == INFINITY ? 0.0f : fa - ha, __builtin_fabsf(hb) == INFINITY ? 0.0f : fb - hb);
-      } else {
-        const float ca = bf16_cut(a), cb = bf16_cut(b);
-        hi = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u);
-        if (a != a) hi |= 0x7fc0u;                                       // a NaN whose top bits are an infinity's
-        if (b != b) hi |= 0x7fc00000u;
-        lo = pack_half2<false>(bf16_rest(a, ca), bf16_rest(b, cb));
-      }
-      uint8_t* d = vt + i * pitch + (rank >> 4) * 64 + (rank & 15) * 2;
-      *reinterpret_cast<uint32_t*>(d) = hi;
-      *reinterpret_cast<uint32_t*>(d + 32) = lo;
-    }
-    if (x == 0) fac[i] = back;
+  __device__ __forceinline__ void find(const ExpandArgs& p, const GroupTile& t, int place0) {
+    place = place0 + (threadIdx.x & 15);
+    tok = place < t.row_end ? token_at(p.pl, place) : -1;
+    factor = back = 1.0f;
   }
-  __syncthreads();
-
-  int64_t tok[MF];
-  float back[MF];
+  // v of ranks 16 (s0 + s) + 8 (q % 2) .. + 7
+  __device__ __forceinline__ void fetch(const ExpandArgs& p, int s0, v4f (&v)[STEPS][2]) const {
+    const int h = (threadIdx.x >> 4) & 1;
 #pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int place = t.row0 + 16 * i + x;
-    tok[i] = place < t.row_end ? token_at(p.pl, place) : -1;
-    back[i] = F16 ? fac[16 * i + x] : 1.0f;
-  }
-  const uint16_t* wg = p.w + (int64_t)t.g * p.r * p.n;
-  for (int n0 = c0 + w * 64; n0 < c1; n0 += 256) {
-    // columns of a lane: 32 jp + 8 q .. + 7; a fragment j of a pair has 8 (x / 4) + 4 j + x % 4
-    v4i bs[2][MF];
+    for (int s = 0; s < STEPS; ++s) v[s][0] = v[s][1] = v4f{0, 0, 0, 0};
+    for (int e = 0; e < p.slices; e += 2) {
+      v4f in[2][STEPS][2];
 #pragma unroll
-    for (int jp = 0; jp < 2; ++jp)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        const int col = n0 + 32 * jp + 8 * q;
-        bs[jp][i] = v4i{0, 0, 0, 0};
-        if (p.base != nullptr && tok[i] >= 0 && col < c1) bs[jp][i] = load8(p.base + tok[i] * p.n + col);
-      }
-    v4f acc[MF][4];
-#pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    const uint16_t* wp[4];
-    if constexpr (!WT) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = n0 + 32 * (j >> 1) + 8 * (x >> 2) + 4 * (j & 1) + (x & 3);
-        wp[j] = wg + (int64_t)(col < c1 ? col : c1 - 1) * p.r + 8 * (q & 1);
-      }
-    }
-    for (int s = 0; s < steps; ++s) {
-      if constexpr (WT) {
-        if (s % (kWtRanks / 16) == 0) {
-          // the next ranks' rows of 64 columns into the wave's share: 8 lanes a row
-          asm volatile("" ::: "memory");
-          const int ranks = p.r - 16 * s < kWtRanks ? p.r - 16 * s : kWtRanks;
-          for (int row = lane >> 3; row < (ranks + 15) / 16 * 16; row += 8) {
-            const int col = n0 + (lane & 7) * 8;
-            v4i v = v4i{0, 0, 0, 0};
-            if (row < ranks && col < c1) v = load8(wg + (int64_t)(16 * s + row) * p.n + col);
-            *reinterpret_cast<v4i*>(wt + row * 144 + (lane & 7) * 16) = v;
+        for (int s = 0; s < STEPS; ++s) {
+          in[i][s][0] = in[i][s][1] = v4f{0, 0, 0, 0};
+          const int rank = 16 * (s0 + s) + 8 * h;
+          if (tok >= 0 && rank < p.r && e + i < p.slices) {
+            const v4f* src = reinterpret_cast<const v4f*>(p.v + ((int64_t)(e + i) * p.pl.max_rows + place) * p.r + rank);
+            in[i][s][0] = src[0];
+            in[i][s][1] = src[1];
           }
-          asm volatile("" ::: "memory");
         }
-      }
-      v4i wf[4], vf[MF];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (WT) {
-          const uint8_t* at = wt + (s % (kWtRanks / 16) * 16 + 8 * (q & 1) + (x >> 2)) * 144 +
-                              (32 * (j >> 1) + 8 * (x & 3) + 4 * (j & 1)) * 2;
-          wf[j] = join(read_transposed(at), read_transposed(at + 4 * 144));
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          v[s][0] += in[i][s][0];
+          v[s][1] += in[i][s][1];
+        }
+    }
+  }
+  // FP16: takes these ranks into the place's largest value
+  __device__ __forceinline__ void largest(const v4f (&v)[STEPS][2], float scale, uint32_t& top) const {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t a = __float_as_uint(v[s][e >> 2][e & 3] * scale) & 0x7fffffffu;
+        top = a > top ? a : top;
+      }
+  }
+  __device__ __forceinline__ void set_factor(uint32_t top) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, 16, 64);           // the other half of the ranks
+    top = o > top ? o : top;
+    int e = (int)(top >> 23);                                            // biased exponent
+    e = e < 15 ? 15 : (e > 254 ? 141 : e);                               // Inf and NaN: unscaled
+    factor = __uint_as_float((uint32_t)(127 + 141 - e) << 23);
+    back = __uint_as_float((uint32_t)(127 - 141 + e) << 23);
+  }
+  __device__ __forceinline__ void split(const v4f (&v)[STEPS][2], float scale) {
+    const bool low = (threadIdx.x & 32) != 0;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = v[s][e >> 1][2 * (e & 1)] * scale, b = v[s][e >> 1][2 * (e & 1) + 1] * scale;
+        uint32_t hi, lo;
+        if constexpr (F16) {
+          const float fa = a * factor, fb = b * factor;
+          hi = pack_half2<true>(fa, fb);
+          const float ha = f16_lo(hi), hb = f16_hi(hi);
+          lo = pack_half2<true>(__builtin_fabsf(ha) == INFINITY ? 0.0f : fa - ha, __builtin_fabsf(hb) == INFINITY ? 0.0f : fb - hb);
         } else {
-          wf[j] = v4i{0, 0, 0, 0};
-          if (16 * s + 8 * (q & 1) < p.r) wf[j] = load8(wp[j] + 16 * s);
+          hi = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u);
+          if (a != a) hi |= 0x7fc0u;                                     // a NaN whose top bits are an infinity's
+          if (b != b) hi |= 0x7fc00000u;
+          lo = pack_half2<false>(bf16_rest(a, bf16_cut(a)), bf16_rest(b, bf16_cut(b)));
+        }
+        part[s][e] = (int)(low ? lo : hi);
+      }
+  }
+  // the fragments of the ranks from 16 s0 on
+  __device__ __forceinline__ void load(const ExpandArgs& p, float scale, int s0) {
+    v4f v[STEPS][2];
+    fetch(p, s0, v);
+    split(v, scale);
+  }
+  // FP16: the factor, and all fragments where the ranks are no more than STEPS hold
+  __device__ __forceinline__ void start(const ExpandArgs& p, float scale, bool keep_v) {
+    v4f v[STEPS][2];
+    uint32_t top = 0;
+    for (int s0 = 0; 16 * s0 < p.r; s0 += STEPS) {
+      fetch(p, s0, v);
+      if constexpr (F16) largest(v, scale, top);
+      if (keep_v && tok >= 0 && (threadIdx.x & 32) == 0) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const int rank = 16 * (s0 + s) + 8 * ((threadIdx.x >> 4) & 1);
+          if (rank < p.r) {
+            v4f* d = reinterpret_cast<v4f*>(p.v_out + (int64_t)place * p.r + rank);
+            d[0] = v[s][0];
+            d[1] = v[s][1];
+          }
         }
       }
+    }
+    if constexpr (F16) set_factor(top);
+    if (p.r <= 16 * STEPS) split(v, scale);
+  }
+};
+
+// Eight results of a lane: columns n .. + 7 of its place's token.
+template <bool F16>
+__device__ __forceinline__ void expand_store(uint16_t* d, v4i base, v4f a, v4f b, float back) {
+  const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  v4i o;
 #pragma unroll
-      for (int i = 0; i < MF; ++i) vf[i] = *reinterpret_cast<const v4i*>(vt + (16 * i + x) * pitch + s * 64 + q * 16);
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t u = (uint32_t)base[e];
+    o[e] = (int)pack_half2<F16>(__builtin_fmaf(f[2 * e], back, half_lo<F16>(u)),
+                                __builtin_fmaf(f[2 * e + 1], back, half_hi<F16>(u)));
+  }
+  *reinterpret_cast<v4i*>(d) = o;
+}
+
+// The columns of fragment j of a lane's pairs: 32 (j / 2) + 8 (x / 4) + 4 (j % 2) + x %
+// 4, so that a pair's sums are eight neighbouring columns 32 (j / 2) + 8 q .. + 7.
+__device__ __forceinline__ int pair_column(int j, int x) { return 32 * (j >> 1) + 8 * (x >> 2) + 4 * (j & 1) + (x & 3); }
+
+// Few places an adapter: a workgroup has 16 of them, each wave 64 of every 256
+// columns, with the weights straight from memory (WT: through the wave's share of
+// LDS, 64 ranks at a time, read transposed).
+constexpr int kFewPitch = 144;
+template <bool F16, bool WT, int STEPS>
+__device__ __forceinline__ void expand_few(const ExpandArgs& p, int id) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), x = lane & 15, q = lane >> 4;
+  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 16, id / p.chunks);
+  if (t.g < 0) return;
+  const int c0 = id % p.chunks * p.chunk, c1 = c0 + p.chunk < p.n ? c0 + p.chunk : p.n;
+  const float scale = p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
+  uint8_t* wt = smem + w * 16 * STEPS * kFewPitch;
+  const uint16_t* wg = p.w + (int64_t)t.g * p.r * p.n;
+  Places<F16, STEPS> pl;
+  pl.find(p, t, t.row0);
+  pl.start(p, scale, p.v_out != nullptr && c0 == 0 && w == 0);
+  for (int n0 = c0 + w * 64; n0 < c1; n0 += 256) {
+    v4i base[2];
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
+    for (int jp = 0; jp < 2; ++jp) {
+      const int col = n0 + 32 * jp + 8 * q;
+      base[jp] = v4i{0, 0, 0, 0};
+      if (p.base != nullptr && pl.tok >= 0 && col < c1) base[jp] = load8(p.base + pl.tok * p.n + col);
+    }
+    v4f acc[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = product16<F16>(wf[j], vf[i], acc[i][j]);
+    for (int j = 0; j < 4; ++j) acc[j] = v4f{0, 0, 0, 0};
+    for (int s0 = 0; 16 * s0 < p.r; s0 += STEPS) {
+      if (p.r > 16 * STEPS) pl.load(p, scale, s0);
+      v4i wf[STEPS][4];
+      if constexpr (WT) {
+        // 16 STEPS rows of 64 columns: 8 lanes a row
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int e = 0; e < 2 * STEPS; ++e) {
+          const int row = (lane >> 3) + 8 * e, col = n0 + (lane & 7) * 8;
+          v4i v = v4i{0, 0, 0, 0};
+          if (16 * s0 + row < p.r && col < c1) v = load8(wg + (int64_t)(16 * s0 + row) * p.n + col);
+          *reinterpret_cast<v4i*>(wt + row * kFewPitch + (lane & 7) * 16) = v;
+        }
+        asm volatile("" ::: "memory");
+      }
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (WT) {
+            const uint8_t* at = wt + (16 * s + 8 * (q & 1) + (x >> 2)) * kFewPitch + (32 * (j >> 1) + 8 * (x & 3) + 4 * (j & 1)) * 2;
+            wf[s][j] = join(read_transposed(at), read_transposed(at + 4 * kFewPitch));
+          } else {
+            const int col = n0 + pair_column(j, x), rank = 16 * (s0 + s) + 8 * (q & 1);
+            wf[s][j] = v4i{0, 0, 0, 0};
+            if (rank < p.r) wf[s][j] = load8(wg + (int64_t)(col < c1 ? col : c1 - 1) * p.r + rank);
+          }
+        }
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = product16<F16>(wf[s][j], pl.part[s], acc[j]);
     }
 #pragma unroll
-    for (int jp = 0; jp < 2; ++jp)
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        const int col = n0 + 32 * jp + 8 * q;
-        if (tok[i] < 0 || col >= c1) continue;
-        const v4f a = acc[i][2 * jp], b = acc[i][2 * jp + 1];
-        const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        v4i o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t u = (uint32_t)bs[jp][i][e];
-          o[e] = (int)pack_half2<F16>(__builtin_fmaf(f[2 * e], back[i], half_lo<F16>(u)),
-                                      __builtin_fmaf(f[2 * e + 1], back[i], half_hi<F16>(u)));
-        }
-        *reinterpret_cast<v4i*>(p.out + tok[i] * p.n + col) = o;
-      }
+    for (int jp = 0; jp < 2; ++jp) {
+      const int col = n0 + 32 * jp + 8 * q;
+      if (pl.tok >= 0 && col < c1)
+        expand_store<F16>(p.out + pl.tok * p.n + col, base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
+    }
   }
 }
 
-template <bool F16, int MF>
-__global__ __launch_bounds__(kThreads) void lora_expand(ExpandArgs p) {
-  if (blockIdx.x < p.tiles) expand_tile<F16, false, MF>(p, blockIdx.x);
-  else expand_rest(p, (int)(blockIdx.x - p.tiles));
+// Many places: a workgroup has 64 of them, 16 a wave, and goes through its columns
+// 256 at a time, so that a row's loads and stores are 512 bytes.  The weights of a
+// block of columns (and of 16 STEPS ranks) lie in one of two LDS buffers, which
+// the waves fill together from registers that the next block's are loaded into
+// meanwhile.
+template <bool WT, int STEPS>
+struct ManyCfg {
+  static constexpr int SS = STEPS < 2 ? STEPS : 2;         // steps of a stage
+  static constexpr int PITCH = WT ? 528 : SS * 32 + 16;
+  static constexpr int BUF = WT ? 16 * SS * PITCH : 256 * PITCH;
+};
+template <bool F16, bool WT, int STEPS>
+__device__ __forceinline__ void expand_many(const ExpandArgs& p, int id) {
+  using M = ManyCfg<WT, STEPS>;
+  constexpr int PITCH = M::PITCH, SS = M::SS, PCS = 2 * SS;         // PCS: 16-byte pieces of a thread
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), x = lane & 15, q = lane >> 4;
+  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 64, id / p.chunks);
+  if (t.g < 0) return;
+  const int c0 = id % p.chunks * p.chunk, c1 = c0 + p.chunk < p.n ? c0 + p.chunk : p.n;
+  const float scale = p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
+  const uint16_t* wg = p.w + (int64_t)t.g * p.r * p.n;
+  v4i piece[PCS];
+  auto fetch = [&](int n0, int s0) {
+#pragma unroll
+    for (int e = 0; e < PCS; ++e) {
+      const int c = tid + 256 * e;
+      piece[e] = v4i{0, 0, 0, 0};
+      if constexpr (WT) {
+        const int row = 16 * s0 + (c >> 5), col = n0 + (c & 31) * 8;
+        if (row < p.r && col < c1) piece[e] = load8(wg + (int64_t)row * p.n + col);
+      } else {
+        const int col = n0 + c / PCS, rank = 16 * s0 + c % PCS * 8;
+        if (rank < p.r && col < c1) piece[e] = load8(wg + (int64_t)col * p.r + rank);
+      }
+    }
+  };
+  fetch(c0, 0);
+  Places<F16, STEPS> pl;
+  pl.find(p, t, t.row0 + 16 * w);
+  pl.start(p, scale, false);
+  int buf = 0;
+  for (int n0 = c0; n0 < c1; n0 += 256) {
+    v4i base[8];
+#pragma unroll
+    for (int jp = 0; jp < 8; ++jp) {
+      const int col = n0 + 32 * jp + 8 * q;
+      base[jp] = v4i{0, 0, 0, 0};
+      if (p.base != nullptr && pl.tok >= 0 && col < c1) base[jp] = load8(p.base + pl.tok * p.n + col);
+    }
+    v4f acc[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = v4f{0, 0, 0, 0};
+    for (int s0 = 0; 16 * s0 < p.r; s0 += STEPS) {
+      if (p.r > 16 * STEPS) pl.load(p, scale, s0);
+#pragma unroll
+      for (int s1 = 0; s1 < STEPS; s1 += SS) {
+        if (16 * (s0 + s1) >= p.r) break;
+        uint8_t* b = smem + buf * M::BUF;
+        buf ^= 1;
+#pragma unroll
+        for (int e = 0; e < PCS; ++e) {
+          const int c = tid + 256 * e;
+          *reinterpret_cast<v4i*>(b + (WT ? (c >> 5) * PITCH + (c & 31) * 16 : c / PCS * PITCH + c % PCS * 16)) = piece[e];
+        }
+        if (16 * (s0 + s1 + SS) < p.r) fetch(n0, s0 + s1 + SS);
+        else if (n0 + 256 < c1) fetch(n0 + 256, 0);
+        // the buffer is written; its readers of two stages ago are past the barrier in between
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int s = 0; s < SS; ++s)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            v4i wf;
+            if constexpr (WT) {
+              const uint8_t* at = b + (16 * s + 8 * (q & 1) + (x >> 2)) * PITCH + (32 * (j >> 1) + 8 * (x & 3) + 4 * (j & 1)) * 2;
+              wf = join(read_transposed(at), read_transposed(at + 4 * PITCH));
+            } else {
+              wf = *reinterpret_cast<const v4i*>(b + pair_column(j, x) * PITCH + s * 32 + (q & 1) * 16);
+            }
+            acc[j] = product16<F16>(wf, pl.part[s1 + s], acc[j]);
+            if (j % 8 == 7) __builtin_amdgcn_sched_barrier(0);       // no more fragments under way than registers hold
+          }
+      }
+    }
+#pragma unroll
+    for (int jp = 0; jp < 8; ++jp) {
+      const int col = n0 + 32 * jp + 8 * q;
+      if (pl.tok >= 0 && col < c1)
+        expand_store<F16>(p.out + pl.tok * p.n + col, base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
+    }
+  }
+}
+
+template <bool F16, bool WT, int STEPS, bool MANY>
+__global__ __launch_bounds__(kThreads, 2) void lora_expand(ExpandArgs p) {
+  if (blockIdx.x >= p.tiles) expand_rest(p, (int)(blockIdx.x - p.tiles));
+  else if constexpr (MANY) expand_many<F16, WT, STEPS>(p, (int)blockIdx.x);
+  else expand_few<F16, WT, STEPS>(p, (int)blockIdx.x);
 }
 
 // ------------------------------------------------------------------ outer
@@ -498,20 +651,14 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
     }
 }
 
-// dx, dA's and dB's chunks in one launch: the longest first.
+// dA's and dB's chunks in one launch.
 struct BackArgs {
-  ExpandArgs dx;           // tiles and rest 0: no dx
   OuterArgs da, db;
 };
-template <bool F16, int MF, int RF>
-__global__ __launch_bounds__(kThreads) void lora_back(BackArgs p) {
-  unsigned id = blockIdx.x;
-  if (id < p.da.tiles) return outer_tile<F16, false, RF>(p.da, (int)id);
-  id -= p.da.tiles;
-  if (id < p.db.tiles) return outer_tile<F16, true, RF>(p.db, (int)id);
-  id -= p.db.tiles;
-  if (id < p.dx.tiles) return expand_tile<F16, true, MF>(p.dx, (int)id);
-  expand_rest(p.dx, (int)(id - p.dx.tiles));
+template <bool F16, int RF>
+__global__ __launch_bounds__(kThreads) void lora_outer(BackArgs p) {
+  if (blockIdx.x < p.da.tiles) outer_tile<F16, false, RF>(p.da, (int)blockIdx.x);
+  else outer_tile<F16, true, RF>(p.db, (int)(blockIdx.x - p.da.tiles));
 }
 
 // da, db: scale times the sum of an adapter's chunks, in order.
@@ -550,25 +697,38 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t tile_bound(int64_t max_rows, int64_t adapters, int64_t bm) {
   return max_rows / bm + (max_rows < adapters ? max_rows : adapters);
 }
-constexpr int64_t kFill = 512;           // workgroups that fill the chip
+#ifndef XF
+#define XF 512
+#endif
+constexpr int64_t kFill = XF;           // workgroups that fill the chip
 
-int shrink_mf(int64_t max_rows, int64_t adapters) { return max_rows > 16 * adapters ? 2 : 1; }
-int shrink_rf(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
-int shrink_slices(int64_t max_rows, int64_t adapters, int64_t k, int64_t r) {
-  const int64_t wgs = tile_bound(max_rows, adapters, 16 * shrink_mf(max_rows, adapters)) * up(r, 16 * shrink_rf(r));
-  const int64_t most = up(k, 512);       // a block of 64 for each wave
+// Few places an adapter: tiles of 16.  More: of 64, of 128 where those fill the chip.
+struct ShrinkPlan {
+  int rw, mf, rf, slices;
+  int64_t tiles;                         // of places
+  bool summed() const { return rw > 1 && slices > 1; }       // by lora_slices; else by the readers
+};
+ShrinkPlan shrink_plan(int64_t max_rows, int64_t adapters, int64_t k, int64_t r) {
+  ShrinkPlan p{1, 1, r <= 16 ? 1 : r <= 32 ? 2 : 4, 1, 0};
+  if (max_rows > 16 * adapters) p.rw = 4;
+  if (p.rw == 4 && max_rows / 128 >= kFill / 4) p.mf = 2;
+  p.tiles = tile_bound(max_rows, adapters, 16 * p.rw * p.mf);
+  const int64_t wgs = p.tiles * up(r, 16 * p.rf), most = up(k, 64 * kShrinkWaves / p.rw);
   int64_t s = wgs > 0 ? kFill / wgs : 1;
   s = s < most ? s : most;
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+  p.slices = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+  return p;
 }
-int expand_mf(int64_t max_rows, int64_t adapters, int64_t r) {
-  return r > 256 || max_rows <= 16 * adapters ? 1 : r > 128 || max_rows <= 64 * adapters ? 2 : 4;
-}
-// Columns of a workgroup: 256, more where that leaves enough workgroups.
+// Places of a workgroup: 16 where an adapter has few on average, else 64.
+int expand_places(int64_t max_rows, int64_t adapters) { return max_rows <= 16 * adapters ? 16 : 64; }
+int expand_steps(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
+// Columns of a workgroup: what makes about kFill workgroups, whole 256s.
 int expand_chunk(int64_t tiles, int64_t n) {
-  int64_t c = 256;
-  while (c < 4096 && c < n && tiles * up(n, 2 * c) >= 2 * kFill) c *= 2;
-  return (int)c;
+  #ifndef XE
+#define XE 512
+#endif
+  const int64_t across = tiles > 0 ? up(XE, tiles) : 1;
+  return (int)(up(up(n, across), 256) * 256);
 }
 int outer_rf(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 // Places of a chunk of dA and dB: about 2 kFill workgroups.
@@ -592,104 +752,123 @@ hipError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&set)[64]) {
   return e;
 }
 
-template <bool F16, bool WT, int MF, int RF>
-hipError_t shrink_one(hipStream_t s, const ShrinkArgs& p) {
+template <bool F16, bool WT, int RW, int MF, int RF>
+hipError_t shrink_one(hipStream_t s, const ShrinkArgs& p, const ShrinkPlan& plan) {
   constexpr int kSum = kShrinkWaves * MF * RF * 1024, kW = WT ? kShrinkWaves * 64 * (RF * 32 + 16) : 0;
   constexpr int bytes = kSum > kW ? kSum : kW;
-  const int64_t wgs = tile_bound(p.pl.max_rows, p.pl.adapters, 16 * MF) * up(p.r, 16 * RF) * p.slices;
+  const int64_t wgs = plan.tiles * up(p.r, 16 * RF) * p.slices;
   static std::atomic<bool> set[64];
-  const hipError_t e = allow_smem(lora_shrink<F16, WT, MF, RF>, bytes, set);
+  const hipError_t e = allow_smem(lora_shrink<F16, WT, RW, MF, RF>, bytes, set);
   if (e != hipSuccess || wgs == 0) return e;
-  hipLaunchKernelGGL((lora_shrink<F16, WT, MF, RF>), dim3((unsigned)wgs), dim3(kShrinkWaves * 64), bytes, s, p);
+  hipLaunchKernelGGL((lora_shrink<F16, WT, RW, MF, RF>), dim3((unsigned)wgs), dim3(kShrinkWaves * 64), bytes, s, p);
   return hipGetLastError();
 }
+template <bool F16, bool WT, int RW, int MF>
+hipError_t shrink_rf(hipStream_t s, const ShrinkArgs& p, const ShrinkPlan& plan) {
+  return plan.rf == 1 ? shrink_one<F16, WT, RW, MF, 1>(s, p, plan)
+         : plan.rf == 2 ? shrink_one<F16, WT, RW, MF, 2>(s, p, plan)
+                        : shrink_one<F16, WT, RW, MF, 4>(s, p, plan);
+}
+// z w^T into `out` [max_rows, r], or, where the plan leaves the slices to the
+// readers, [slices, max_rows, r]; `parts` holds the slices where they are summed here.
 template <bool F16, bool WT>
-hipError_t shrink(hipStream_t s, const ShrinkArgs& p) {
-  const int mf = shrink_mf(p.pl.max_rows, p.pl.adapters), rf = shrink_rf(p.r);
-  if (mf == 1) return rf == 1 ? shrink_one<F16, WT, 1, 1>(s, p) : rf == 2 ? shrink_one<F16, WT, 1, 2>(s, p) : shrink_one<F16, WT, 1, 4>(s, p);
-  return rf == 1 ? shrink_one<F16, WT, 2, 1>(s, p) : rf == 2 ? shrink_one<F16, WT, 2, 2>(s, p) : shrink_one<F16, WT, 2, 4>(s, p);
+hipError_t shrink(hipStream_t s, const LoraPlan& pl, const uint16_t* z, const uint16_t* w, int64_t k, int64_t r,
+                  const ShrinkPlan& plan, float* parts, float* out) {
+  const ShrinkArgs p{pl, z, w, plan.summed() ? parts : out, (int)k, (int)r, plan.slices};
+  const hipError_t e = plan.rw == 1   ? shrink_rf<F16, WT, 1, 1>(s, p, plan)
+                       : plan.mf == 1 ? shrink_rf<F16, WT, 4, 1>(s, p, plan)
+                                      : shrink_rf<F16, WT, 4, 2>(s, p, plan);
+  if (e != hipSuccess || !plan.summed()) return e;
+  hipLaunchKernelGGL(lora_slices, dim3((unsigned)up(pl.max_rows * r, 1024)), dim3(256), 0, s, pl, parts, (int)r, plan.slices, out);
+  return hipGetLastError();
 }
 
 ExpandArgs expand_args(const LoraPlan& pl, const float* v, const uint16_t* w, const uint16_t* base, uint16_t* out,
                        float* v_out, int64_t n, int64_t r, int slices) {
-  ExpandArgs p{pl, v, w, base, out, v_out, (int)n, (int)r, slices, 0, 0, 0, 0};
-  const int64_t tiles = tile_bound(pl.max_rows, pl.adapters, 16 * expand_mf(pl.max_rows, pl.adapters, r));
+  ExpandArgs p{pl, v, w, base, out, v_out, (int)n, (int)r, slices, 0, 0, 0, 0, 0};
+  const int64_t tiles = tile_bound(pl.max_rows, pl.adapters, expand_places(pl.max_rows, pl.adapters));
   p.chunk = expand_chunk(tiles, n);
   p.chunks = (int)up(n, p.chunk);
   p.tiles = (unsigned)(tiles * p.chunks);
-  p.rest = base != out ? (unsigned)(up(pl.m, kRestRows) * p.chunks) : 0;
+  const int64_t rest = up(pl.m, kRestRows);
+  p.rest_chunks = (int)up(n, kRestCols);
+  p.rest = base != out ? (unsigned)(rest * p.rest_chunks) : 0;
   return p;
 }
 
-template <bool F16, int MF>
+template <bool F16, bool WT, int STEPS, bool MANY>
 hipError_t expand_one(hipStream_t s, const ExpandArgs& p) {
-  const int bytes = expand_smem<false, MF>(p.r);
-  if (p.tiles + p.rest == 0) return hipSuccess;
-  hipLaunchKernelGGL((lora_expand<F16, MF>), dim3(p.tiles + p.rest), dim3(kThreads), bytes, s, p);
+  constexpr int bytes = MANY ? 2 * ManyCfg<WT, STEPS>::BUF : WT ? 4 * 16 * STEPS * kFewPitch : 0;
+  static std::atomic<bool> set[64];
+  const hipError_t e = allow_smem(lora_expand<F16, WT, STEPS, MANY>, bytes, set);
+  if (e != hipSuccess || p.tiles + p.rest == 0) return e;
+  hipLaunchKernelGGL((lora_expand<F16, WT, STEPS, MANY>), dim3(p.tiles + p.rest), dim3(kThreads), bytes, s, p);
   return hipGetLastError();
+}
+template <bool F16, bool WT, int STEPS>
+hipError_t expand_steps(hipStream_t s, const ExpandArgs& p) {
+  return expand_places(p.pl.max_rows, p.pl.adapters) == 16 ? expand_one<F16, WT, STEPS, false>(s, p)
+                                                          : expand_one<F16, WT, STEPS, true>(s, p);
+}
+template <bool F16, bool WT>
+hipError_t expand(hipStream_t s, const ExpandArgs& p) {
+  const int steps = expand_steps(p.r);
+  return steps == 1 ? expand_steps<F16, WT, 1>(s, p) : steps == 2 ? expand_steps<F16, WT, 2>(s, p) : expand_steps<F16, WT, 4>(s, p);
 }
 template <bool F16>
 hipError_t forward(hipStream_t s, const LoraArgs& p) {
   const LoraPlan& pl = p.plan;
-  const int slices = shrink_slices(pl.max_rows, pl.adapters, p.k, p.r);
-  float* v = slices == 1 && p.v != nullptr ? p.v : static_cast<float*>(p.workspace);
-  const hipError_t e = shrink<F16, false>(s, ShrinkArgs{pl, p.x, p.a, v, (int)p.k, (int)p.r, slices});
+  const ShrinkPlan plan = shrink_plan(pl.max_rows, pl.adapters, p.k, p.r);
+  // the workspace: the slices (if any), then v where it is not kept
+  float* parts = static_cast<float*>(p.workspace);
+  const bool several = plan.slices > 1 && !plan.summed();
+  float* v = several ? parts : p.v != nullptr ? p.v : parts + (plan.summed() ? plan.slices * pl.max_rows * p.r : 0);
+  const hipError_t e = shrink<F16, false>(s, pl, p.x, p.a, p.k, p.r, plan, parts, v);
   if (e != hipSuccess) return e;
-  const ExpandArgs x = expand_args(pl, v, p.b, p.base, p.out, v != p.v ? p.v : nullptr, p.n, p.r, slices);
-  switch (expand_mf(pl.max_rows, pl.adapters, p.r)) {
-    case 1: return expand_one<F16, 1>(s, x);
-    case 2: return expand_one<F16, 2>(s, x);
-    default: return expand_one<F16, 4>(s, x);
-  }
+  const ExpandArgs x = expand_args(pl, v, p.b, p.base, p.out, several ? p.v : nullptr, p.n, p.r, several ? plan.slices : 1);
+  return expand<F16, false>(s, x);
 }
 
-template <bool F16, int MF, int RF>
-hipError_t back_one(hipStream_t s, const BackArgs& p) {
-  const int a = expand_smem<true, MF>(p.dx.r), b = outer_smem<RF>(), bytes = a > b ? a : b;
-  const unsigned wgs = p.da.tiles + p.db.tiles + p.dx.tiles + p.dx.rest;
-  static std::atomic<bool> set[64];
-  const hipError_t e = allow_smem(lora_back<F16, MF, RF>, bytes > 65536 ? 163840 : bytes, set);
-  if (e != hipSuccess || wgs == 0) return e;
-  hipLaunchKernelGGL((lora_back<F16, MF, RF>), dim3(wgs), dim3(kThreads), bytes, s, p);
+// Floats of slices and sums of a shrink in the workspace.
+uint64_t shrink_space(const ShrinkPlan& p, int64_t max_rows, int64_t r) {
+  return (uint64_t)(p.slices + (p.summed() ? 1 : 0)) * max_rows * r;
+}
+uint64_t chunk_count(int64_t max_rows, int64_t n, int64_t k, int64_t r, int64_t adapters) {
+  return (uint64_t)tile_bound(max_rows, adapters, outer_places(max_rows, n, k, r));
+}
+
+template <bool F16, int RF>
+hipError_t outer(hipStream_t s, const BackArgs& p) {
+  const unsigned wgs = p.da.tiles + p.db.tiles;
+  if (wgs == 0) return hipSuccess;
+  hipLaunchKernelGGL((lora_outer<F16, RF>), dim3(wgs), dim3(kThreads), outer_smem<RF>(), s, p);
   return hipGetLastError();
-}
-template <bool F16, int MF>
-hipError_t back(hipStream_t s, const BackArgs& p) {
-  const int rf = outer_rf(p.dx.r);
-  return rf == 1 ? back_one<F16, MF, 1>(s, p) : rf == 2 ? back_one<F16, MF, 2>(s, p) : back_one<F16, MF, 4>(s, p);
-}
-
-struct BackSpace {
-  uint64_t u, da, db;      // bytes
-};
-BackSpace back_space(int64_t max_rows, int64_t n, int64_t k, int64_t r, int64_t adapters) {
-  const int64_t chunks = tile_bound(max_rows, adapters, outer_places(max_rows, n, k, r));
-  return {(uint64_t)shrink_slices(max_rows, adapters, n, r) * max_rows * r * 4, (uint64_t)chunks * r * k * 4,
-          (uint64_t)chunks * r * n * 4};
 }
 
 template <bool F16>
 hipError_t backward(hipStream_t s, const LoraArgs& p) {
   const LoraPlan& pl = p.plan;
-  const BackSpace sp = back_space(pl.max_rows, p.n, p.k, p.r, pl.adapters);
-  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
-  float *u = reinterpret_cast<float*>(ws), *pa = reinterpret_cast<float*>(ws + sp.u), *pb = reinterpret_cast<float*>(ws + sp.u + sp.da);
-  const int slices = shrink_slices(pl.max_rows, pl.adapters, p.n, p.r);
-  hipError_t e = shrink<F16, true>(s, ShrinkArgs{pl, p.dy, p.b, u, (int)p.n, (int)p.r, slices});
+  const ShrinkPlan plan = shrink_plan(pl.max_rows, pl.adapters, p.n, p.r);
+  // the workspace: slices, u, then the chunks of dA and of dB
+  float* parts = static_cast<float*>(p.workspace);
+  float* u = parts + (plan.summed() ? plan.slices * pl.max_rows * p.r : 0);
+  float* pa = parts + shrink_space(plan, pl.max_rows, p.r);
+  float* pb = pa + chunk_count(pl.max_rows, p.n, p.k, p.r, pl.adapters) * p.r * p.k;
+  const int slices = plan.summed() ? 1 : plan.slices;
+  hipError_t e = shrink<F16, true>(s, pl, p.dy, p.b, p.n, p.r, plan, parts, u);
   if (e != hipSuccess) return e;
-  BackArgs x{};
-  x.dx = expand_args(pl, u, p.a, p.base, p.out, nullptr, p.k, p.r, slices);
-  if (p.out == nullptr) x.dx.tiles = x.dx.rest = 0;
   const int places = outer_places(pl.max_rows, p.n, p.k, p.r);
   const int64_t each = tile_bound(pl.max_rows, pl.adapters, places) * up(p.r, 16 * outer_rf(p.r));
+  BackArgs x;
   x.da = OuterArgs{pl, u, p.x, pa, (int)p.k, (int)p.r, slices, places, (unsigned)(each * up(p.k, kOuterCols))};
   x.db = OuterArgs{pl, p.v, p.dy, pb, (int)p.n, (int)p.r, 1, places, (unsigned)(each * up(p.n, kOuterCols))};
-  switch (expand_mf(pl.max_rows, pl.adapters, p.r)) {
-    case 1: e = back<F16, 1>(s, x); break;
-    case 2: e = back<F16, 2>(s, x); break;
-    default: e = back<F16, 4>(s, x); break;
-  }
+  const int rf = outer_rf(p.r);
+  e = rf == 1 ? outer<F16, 1>(s, x) : rf == 2 ? outer<F16, 2>(s, x) : outer<F16, 4>(s, x);
   if (e != hipSuccess) return e;
+  if (p.out != nullptr) {
+    e = expand<F16, true>(s, expand_args(pl, u, p.a, p.base, p.out, nullptr, p.k, p.r, slices));
+    if (e != hipSuccess) return e;
+  }
   SumArgs m{pl, pa, pb, p.da, p.db, p.r * p.k, p.r * p.n, places, (unsigned)up(p.r * (p.k + p.n), 4 * kThreads), p.accumulate};
   hipLaunchKernelGGL(lora_sum, dim3(m.blocks * (unsigned)pl.adapters), dim3(kThreads), 0, s, m);
   return hipGetLastError();
@@ -704,28 +883,28 @@ int64_t lora_work_items(int64_t max_rows, int64_t m, int64_t n, int64_t k, int64
     most = v > most ? v : most;
   };
   int64_t most = 0;
-  const int64_t tiles = tile_bound(max_rows, adapters, 16 * expand_mf(max_rows, adapters, r));
+  const int64_t tiles = tile_bound(max_rows, adapters, expand_places(max_rows, adapters));
   const int64_t places = outer_places(max_rows, n, k, r), chunks = tile_bound(max_rows, adapters, places);
-  for (const int64_t inner : {n, k})
-    more(most, tile_bound(max_rows, adapters, 16 * shrink_mf(max_rows, adapters)) * up(r, 16 * shrink_rf(r)) *
-                   shrink_slices(max_rows, adapters, inner, r), kShrinkWaves * 64);
-  int64_t back = chunks * up(r, 16 * outer_rf(r)) * (up(n, kOuterCols) + up(k, kOuterCols));
-  for (const int64_t outer : {n, k}) {
-    const int64_t wgs = (tiles + up(m, kRestRows)) * up(outer, expand_chunk(tiles, outer));
-    more(most, wgs, kThreads);
-    if (outer == k) back += wgs;
+  for (const int64_t inner : {n, k}) {
+    const ShrinkPlan p = shrink_plan(max_rows, adapters, inner, r);
+    more(most, p.tiles * up(r, 16 * p.rf) * p.slices, kShrinkWaves * 64);
   }
-  more(most, back, kThreads);
+  more(most, up(max_rows * r, 1024), 256);
+  for (const int64_t outer : {n, k}) {
+    const int64_t wgs = tiles * up(outer, expand_chunk(tiles, outer)) + up(m, kRestRows) * up(outer, kRestCols);
+    more(most, wgs, kThreads);
+  }
+  more(most, chunks * up(r, 16 * outer_rf(r)) * (up(n, kOuterCols) + up(k, kOuterCols)), kThreads);
   more(most, up(r * (k + n), 4 * kThreads) * adapters, kThreads);
   return most;
 }
 
 uint64_t lora_workspace_bytes(int64_t max_rows, int64_t, int64_t k, int64_t r, int32_t adapters) {
-  return (uint64_t)shrink_slices(max_rows, adapters, k, r) * max_rows * r * 4;
+  return 4 * shrink_space(shrink_plan(max_rows, adapters, k, r), max_rows, r);
 }
 uint64_t lora_backward_workspace_bytes(int64_t max_rows, int64_t n, int64_t k, int64_t r, int32_t adapters) {
-  const BackSpace sp = back_space(max_rows, n, k, r, adapters);
-  return sp.u + sp.da + sp.db;
+  return 4 * (shrink_space(shrink_plan(max_rows, adapters, n, r), max_rows, r) +
+              chunk_count(max_rows, n, k, r, adapters) * (uint64_t)(r * (k + n)));
 }
 
 hipError_t launch_lora(hipStream_t s, const LoraArgs& p) { return p.f16 ? forward<true>(s, p) : forward<false>(s, p); }
