@@ -7,6 +7,7 @@
 #include "group_tiles.hpp"
 #include "half_internal.hpp"
 #include "half_math.hpp"
+#include "tile_util.hpp"
 
 namespace hq {
 namespace {
@@ -22,11 +23,10 @@ __device__ __forceinline__ v4i load8(const uint16_t* p) { return *reinterpret_ca
 // ------------------------------------------------------------------ shrink
 constexpr int kShrinkWaves = 8;
 
-// Partial sums of a workgroup: 16 MF RW places x 16 RF ranks over one slice of K.
-// Its waves are RW groups of places times W / RW that take blocks of 64 K values in
-// turn, each lane loading its operands from memory (w [K, r]: through the wave's
-// share of LDS, read transposed); waves of the same block share w's lines in
-// the first-level cache.  Their sums meet in LDS in the order of the waves.
+// Few places an adapter: partial sums of a workgroup, 16 places x 16 RF ranks over
+// one slice of K.  Its waves take blocks of 64 K values in turn, each lane loading
+// its operands from memory (w [K, r]: through the wave's share of LDS, read
+// transposed), and their sums meet in LDS in the order of the waves.
 struct ShrinkArgs {
   LoraPlan pl;
   const uint16_t* z;       // [m, k]
@@ -35,9 +35,9 @@ struct ShrinkArgs {
   int k, r, slices;
 };
 
-template <bool F16, bool WT, int RW, int MF, int RF>
-__global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
-  constexpr int W = kShrinkWaves, KW = W / RW, RN = 16 * RF, PITCH = RN * 2 + 16;
+template <bool F16, bool WT, int RF>
+__global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink_few(ShrinkArgs p) {
+  constexpr int W = kShrinkWaves, RN = 16 * RF, PITCH = RN * 2 + 16;
   constexpr int U = WT ? 1 : 2;                     // blocks in flight
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), x = lane & 15, q = lane >> 4;
   const int chunks = (p.r + RN - 1) / RN;
@@ -45,18 +45,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
   const int slice = id % p.slices;
   id /= p.slices;
   const int r0 = id % chunks * RN;
-  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 16 * MF * RW, id / chunks);
+  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 16, id / chunks);
   if (t.g < 0) return;
-  const int wk = w / RW, place0 = t.row0 + w % RW * 16 * MF;
-  const uint16_t* zp[MF];
-  bool live[MF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int place = place0 + 16 * i + x;
-    const int64_t tok = place < t.row_end ? token_at(p.pl, place) : -1;
-    live[i] = tok >= 0;
-    zp[i] = p.z + (tok >= 0 ? tok : 0) * p.k + 8 * q;
-  }
+  const int place = t.row0 + x;
+  const int64_t tok = place < t.row_end ? token_at(p.pl, place) : -1;
+  const uint16_t* zp = p.z + (tok >= 0 ? tok : 0) * p.k + 8 * q;
   const uint16_t* wg = p.w + (int64_t)t.g * p.r * p.k;
   const uint16_t* wp[RF];
   if constexpr (!WT) {
@@ -67,14 +60,12 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
     }
   }
   uint8_t* mine = smem + w * 64 * PITCH;
-  v4f acc[MF][RF];
+  v4f acc[RF];
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int j = 0; j < RF; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+  for (int j = 0; j < RF; ++j) acc[j] = v4f{0, 0, 0, 0};
   const int blocks = (p.k + 63) / 64, last = blocks * (slice + 1) / p.slices;
-  for (int b = blocks * slice / p.slices + wk * U; b < last; b += KW * U) {
-    v4i zf[U][2][MF], wf[U][2][RF];
+  for (int b = blocks * slice / p.slices + w * U; b < last; b += W * U) {
+    v4i zf[U][2], wf[U][2][RF];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k0 = (b + u) * 64;
@@ -82,11 +73,8 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bool in = on && k0 + 32 * h + 8 * q < p.k;
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-          zf[u][h][i] = v4i{0, 0, 0, 0};
-          if (in && live[i]) zf[u][h][i] = load8(zp[i] + k0 + 32 * h);
-        }
+        zf[u][h] = v4i{0, 0, 0, 0};
+        if (in && tok >= 0) zf[u][h] = load8(zp + k0 + 32 * h);
         if constexpr (!WT) {
 #pragma unroll
           for (int j = 0; j < RF; ++j) {
@@ -125,24 +113,129 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-          for (int j = 0; j < RF; ++j) acc[i][j] = product16<F16>(wf[u][h][j], zf[u][h][i], acc[i][j]);
+        for (int j = 0; j < RF; ++j) acc[j] = product16<F16>(wf[u][h][j], zf[u][h], acc[j]);
   }
-  v4f* part = reinterpret_cast<v4f*>(smem);         // [W][MF * RF][64]
+  v4f* part = reinterpret_cast<v4f*>(smem);         // [W][RF][64]
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int j = 0; j < RF; ++j) part[(w * MF * RF + i * RF + j) * 64 + lane] = acc[i][j];
+  for (int j = 0; j < RF; ++j) part[(w * RF + j) * 64 + lane] = acc[j];
   __syncthreads();
-  for (int f = wk; f < MF * RF; f += KW) {
-    v4f s = part[(w % RW * MF * RF + f) * 64 + lane];
+  if (w >= RF) return;
+  v4f s = part[w * 64 + lane];
 #pragma unroll
-    for (int e = 1; e < KW; ++e) s += part[((e * RW + w % RW) * MF * RF + f) * 64 + lane];
-    const int place = place0 + 16 * (f / RF) + x, rank = r0 + 16 * (f % RF) + 4 * q;
-    if (place < t.row_end && rank < p.r && token_at(p.pl, place) >= 0)
-      *reinterpret_cast<v4f*>(p.out + ((int64_t)slice * p.pl.max_rows + place) * p.r + rank) = s;
+  for (int e = 1; e < W; ++e) s += part[(e * RF + w) * 64 + lane];
+  const int rank = r0 + 16 * w + 4 * q;
+  if (tok >= 0 && rank < p.r) *reinterpret_cast<v4f*>(p.out + ((int64_t)slice * p.pl.max_rows + place) * p.r + rank) = s;
+}
+
+// Many: 64 places x 16 RF ranks over one slice of K.  Steps of 64 K values come
+// straight into one of kManyStages LDS stages, three ahead of the products: a row's
+// 128 bytes from its token's own address, chunks XOR-swizzled; w from a buffer
+// that ends with it (ranks past r are not stored; values past K are zeros, and
+// z's then any of the row's).  WT: w's rows are ranks of one K value, and its fragments
+// are read transposed.  A wave has 16 places and all the ranks.
+constexpr int kManyStages = 4;
+template <int RF>
+struct ShrinkStage {
+  static constexpr int Z = 64 * 128, W = 16 * RF * 128, BYTES = Z + W;
+  static constexpr int WL = RF < 2 ? 1 : RF / 2, OPS = 2 + WL;          // loads of w, and all, of a wave
+};
+template <bool F16, bool WT, int RF>
+__global__ __launch_bounds__(256) void lora_shrink_many(ShrinkArgs p) {
+  using namespace blk;
+  using S = ShrinkStage<RF>;
+  constexpr int RN = 16 * RF, ST = kManyStages;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), x = lane & 15, q = lane >> 4;
+  const int chunks = (p.r + RN - 1) / RN;
+  int id = blockIdx.x;
+  const int slice = id % p.slices;
+  id /= p.slices;
+  const int r0 = id % chunks * RN;
+  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 64, id / chunks);
+  if (t.g < 0) return;
+  const int blocks = (p.k + 63) / 64, first = blocks * slice / p.slices, steps = blocks * (slice + 1) / p.slices - first;
+  const uint32_t lds0 = ufirst((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)smem);
+
+  // z: load i fills rows (4 i + w) 8 .. + 7, lane j the chunk that belongs at slot j % 8 of row j / 8
+  const int chunk = (lane & 7) ^ ((w * 8 + (lane >> 3)) >> 1 & 7);
+  const uint16_t* zrow[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int place = t.row0 + (4 * i + w) * 8 + (lane >> 3);
+    const int64_t tok = place < t.row_end ? token_at(p.pl, place) : -1;
+    zrow[i] = p.z + (tok >= 0 ? tok : 0) * p.k;
+  }
+  // w: NT rows of 128 bytes, as z; WT 64 rows of RN ranks, 2 RF pieces each
+  const uint8_t* wbase = reinterpret_cast<const uint8_t*>(p.w + (int64_t)t.g * p.r * p.k) + (WT ? r0 * 2 : (int64_t)r0 * p.k * 2);
+  const uint32_t pitch = (uint32_t)(WT ? p.r : p.k) * 2;
+  uint32_t woff[S::WL];
+  int wld[S::WL];                        // the load's number
+#pragma unroll
+  for (int i = 0; i < S::WL; ++i) {
+    wld[i] = RF == 1 ? w & 1 : 4 * i + w;
+    if constexpr (WT) {
+      const int piece = wld[i] * 64 + lane;
+      woff[i] = (uint32_t)(piece / (2 * RF)) * pitch + (uint32_t)(piece % (2 * RF)) * 16;
+    } else {
+      const int row = wld[i] * 8 + (lane >> 3);
+      woff[i] = (uint32_t)row * pitch + (uint32_t)(((lane & 7) ^ (row >> 1 & 7)) * 16);
+    }
+  }
+  int wchunk[S::WL];
+#pragma unroll
+  for (int i = 0; i < S::WL; ++i) wchunk[i] = (lane & 7) ^ ((wld[i] * 8 + (lane >> 3)) >> 1 & 7);
+  auto issue = [&](int step) {
+    const int k0 = (first + step) * 64, kleft = step < steps ? p.k - k0 : 0;
+    const uint32_t at = lds0 + (uint32_t)(step % ST) * S::BYTES;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      dma16_at(zrow[i] + (chunk * 8 < kleft ? k0 + chunk * 8 : 0), at + (uint32_t)(4 * i + w) * 1024);
+    const uint8_t* b = wbase + (WT ? (int64_t)k0 * pitch : k0 * 2);
+    // bytes to the end of w's adapter, of at most 64 rows (NT: RN)
+    const int64_t rest = (WT ? (int64_t)(kleft < 64 ? kleft : 64) * pitch - r0 * 2
+                             : (int64_t)(p.r - r0 < RN ? p.r - r0 : RN) * pitch - k0 * 2);
+    const __amdgpu_buffer_rsrc_t src = rsrc(uniform(b), kleft > 0 ? ufirst((uint32_t)rest) : 0u);
+#pragma unroll
+    for (int i = 0; i < S::WL; ++i)
+      dma16(src, WT || wchunk[i] * 8 < kleft ? woff[i] : 0x80000000u, 0, ufirst(at + S::Z + (uint32_t)wld[i] * 1024));
+  };
+#pragma unroll 1
+  for (int s = 0; s < ST - 1; ++s) issue(s);
+
+  v4f acc[RF];
+#pragma unroll
+  for (int j = 0; j < RF; ++j) acc[j] = v4f{0, 0, 0, 0};
+  for (int s = 0; s < steps; ++s) {
+    // this step has landed for every wave, and all have read the one before
+    wait_vm<(ST - 2) * S::OPS>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    bar();
+    issue(s + ST - 1);
+    const uint8_t* at = smem + (s % ST) * S::BYTES;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const v4i zf = *reinterpret_cast<const v4i*>(at + (16 * w + x) * 128 + (((4 * h + q) ^ (x >> 1 & 7)) << 4));
+#pragma unroll
+      for (int j = 0; j < RF; ++j) {
+        v4i wf;
+        if constexpr (WT) {
+          const uint8_t* b = at + S::Z + (32 * h + 8 * q + (x >> 2)) * RN * 2 + (16 * j + 4 * (x & 3)) * 2;
+          wf = join(read_transposed(b), read_transposed(b + 4 * RN * 2));
+        } else {
+          wf = *reinterpret_cast<const v4i*>(at + S::Z + (16 * j + x) * 128 + (((4 * h + q) ^ (x >> 1 & 7)) << 4));
+        }
+        acc[j] = product16<F16>(wf, zf, acc[j]);
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+  wait_vm<0>();           // no load may land in LDS after the workgroup has ended
+  const int place = t.row0 + 16 * w + x;
+  if (place >= t.row_end || token_at(p.pl, place) < 0) return;
+#pragma unroll
+  for (int j = 0; j < RF; ++j) {
+    const int rank = r0 + 16 * j + 4 * q;
+    if (rank < p.r) *reinterpret_cast<v4f*>(p.out + ((int64_t)slice * p.pl.max_rows + place) * p.r + rank) = acc[j];
   }
 }
 
@@ -212,7 +305,7 @@ __device__ __forceinline__ void expand_rest(const ExpandArgs& p, int id) {
 // .. + 7).  BF16: hi is the value cut to 8 bits, lo the rest rounded.  FP16: a
 // place's values are first scaled by the power of two that takes its largest to
 // [2^14, 2^15), undone in FP32 at the end, so that neither part leaves FP16's range.
-template <bool F16, int STEPS>
+template <bool F16, int STEPS, int SL>
 struct Places {
   v4i part[STEPS];
   float factor, back;      // the place's power of two, and the one that undoes it
@@ -229,10 +322,10 @@ struct Places {
     const int h = (threadIdx.x >> 4) & 1;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) v[s][0] = v[s][1] = v4f{0, 0, 0, 0};
-    for (int e = 0; e < p.slices; e += 2) {
-      v4f in[2][STEPS][2];
+    for (int e = 0; e < p.slices; e += SL) {
+      v4f in[SL][STEPS][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < SL; ++i)
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
           in[i][s][0] = in[i][s][1] = v4f{0, 0, 0, 0};
@@ -244,7 +337,7 @@ struct Places {
           }
         }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < SL; ++i)
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
           v[s][0] += in[i][s][0];
@@ -353,52 +446,67 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& p, int id) {
   const float scale = p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
   uint8_t* wt = smem + w * 16 * STEPS * kFewPitch;
   const uint16_t* wg = p.w + (int64_t)t.g * p.r * p.n;
-  Places<F16, STEPS> pl;
+  Places<F16, STEPS, STEPS == 4 ? 2 : 4> pl;
   pl.find(p, t, t.row0);
-  pl.start(p, scale, p.v_out != nullptr && c0 == 0 && w == 0);
-  for (int n0 = c0 + w * 64; n0 < c1; n0 += 256) {
-    v4i base[2];
+  v4i base[2], wf[STEPS][4];
+  auto fetch = [&](int n0, int s0) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        wf[s][j] = v4i{0, 0, 0, 0};
+        if constexpr (WT) {
+          // 16 rows of 64 columns: 8 lanes a row, two loads; the others are not used
+          const int row = 16 * (s0 + s) + (lane >> 3) + 8 * j, col = n0 + (lane & 7) * 8;
+          if (j < 2 && row < p.r && col < c1) wf[s][j] = load8(wg + (int64_t)row * p.n + col);
+        } else {
+          const int col = n0 + pair_column(j, x), rank = 16 * (s0 + s) + 8 * (q & 1);
+          if (rank < p.r) wf[s][j] = load8(wg + (int64_t)(col < c1 ? col : c1 - 1) * p.r + rank);
+        }
+      }
+  };
+  auto fetch_base = [&](int n0) {
 #pragma unroll
     for (int jp = 0; jp < 2; ++jp) {
       const int col = n0 + 32 * jp + 8 * q;
       base[jp] = v4i{0, 0, 0, 0};
       if (p.base != nullptr && pl.tok >= 0 && col < c1) base[jp] = load8(p.base + pl.tok * p.n + col);
     }
+  };
+  pl.start(p, scale, p.v_out != nullptr && c0 == 0 && w == 0);
+  const int first = c0 + w * 64;
+  if (first < c1) {
+    fetch(first, 0);
+    fetch_base(first);
+  }
+  for (int n0 = first; n0 < c1; n0 += 256) {
     v4f acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = v4f{0, 0, 0, 0};
     for (int s0 = 0; 16 * s0 < p.r; s0 += STEPS) {
       if (p.r > 16 * STEPS) pl.load(p, scale, s0);
-      v4i wf[STEPS][4];
       if constexpr (WT) {
-        // 16 STEPS rows of 64 columns: 8 lanes a row
         asm volatile("" ::: "memory");
 #pragma unroll
-        for (int e = 0; e < 2 * STEPS; ++e) {
-          const int row = (lane >> 3) + 8 * e, col = n0 + (lane & 7) * 8;
-          v4i v = v4i{0, 0, 0, 0};
-          if (16 * s0 + row < p.r && col < c1) v = load8(wg + (int64_t)(16 * s0 + row) * p.n + col);
-          *reinterpret_cast<v4i*>(wt + row * kFewPitch + (lane & 7) * 16) = v;
-        }
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<v4i*>(wt + (16 * s + (lane >> 3) + 8 * e) * kFewPitch + (lane & 7) * 16) = wf[s][e];
         asm volatile("" ::: "memory");
       }
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          v4i f = wf[s][j];
           if constexpr (WT) {
             const uint8_t* at = wt + (16 * s + 8 * (q & 1) + (x >> 2)) * kFewPitch + (32 * (j >> 1) + 8 * (x & 3) + 4 * (j & 1)) * 2;
-            wf[s][j] = join(read_transposed(at), read_transposed(at + 4 * kFewPitch));
-          } else {
-            const int col = n0 + pair_column(j, x), rank = 16 * (s0 + s) + 8 * (q & 1);
-            wf[s][j] = v4i{0, 0, 0, 0};
-            if (rank < p.r) wf[s][j] = load8(wg + (int64_t)(col < c1 ? col : c1 - 1) * p.r + rank);
+            f = join(read_transposed(at), read_transposed(at + 4 * kFewPitch));
           }
+          acc[j] = product16<F16>(f, pl.part[s], acc[j]);
         }
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = product16<F16>(wf[s][j], pl.part[s], acc[j]);
+      if (16 * (s0 + STEPS) < p.r) fetch(n0, s0 + STEPS);
+      else if (n0 + 256 < c1) fetch(n0 + 256, 0);
     }
 #pragma unroll
     for (int jp = 0; jp < 2; ++jp) {
@@ -406,6 +514,7 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& p, int id) {
       if (pl.tok >= 0 && col < c1)
         expand_store<F16>(p.out + pl.tok * p.n + col, base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
     }
+    if (n0 + 256 < c1) fetch_base(n0 + 256);
   }
 }
 
@@ -446,9 +555,9 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& p, int id) {
     }
   };
   fetch(c0, 0);
-  Places<F16, STEPS> pl;
+  Places<F16, STEPS, STEPS == 4 ? 1 : 2> pl;
   pl.find(p, t, t.row0 + 16 * w);
-  pl.start(p, scale, false);
+  pl.start(p, scale, p.v_out != nullptr && c0 == 0);
   int buf = 0;
   for (int n0 = c0; n0 < c1; n0 += 256) {
     v4i base[8];
@@ -509,6 +618,121 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand(ExpandArgs p) {
   if (blockIdx.x >= p.tiles) expand_rest(p, (int)(blockIdx.x - p.tiles));
   else if constexpr (MANY) expand_many<F16, WT, STEPS>(p, (int)blockIdx.x);
   else expand_few<F16, WT, STEPS>(p, (int)blockIdx.x);
+}
+
+// ------------------------------------------------------------------ both at once
+// A few places and little to read: one launch.  Every workgroup has 16 places
+// and 1024 columns, 64 a wave; its 16 waves sum x A^T over all of K first, as
+// lora_shrink_few does it, and each takes the sums from LDS as its places' values.
+constexpr int kOneWaves = 16;
+template <bool F16, int STEPS>
+__global__ __launch_bounds__(kOneWaves * 64) void lora_one(ShrinkArgs a, ExpandArgs p) {
+  constexpr int W = kOneWaves, RF = STEPS, U = STEPS == 4 ? 1 : 2, VP = 16 * RF + 4;
+  if (blockIdx.x >= p.tiles) {
+    if (threadIdx.x < 256) expand_rest(p, (int)(blockIdx.x - p.tiles));
+    return;
+  }
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), x = lane & 15, q = lane >> 4;
+  const int id = (int)blockIdx.x;
+  const GroupTile t = group_tile(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, 16, id / p.chunks);
+  if (t.g < 0) return;
+  const float scale = p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
+  Places<F16, STEPS, 1> pl;
+  pl.find(p, t, t.row0);
+  const uint16_t* zp = a.z + (pl.tok >= 0 ? pl.tok : 0) * a.k + 8 * q;
+  const uint16_t* wp[RF];
+#pragma unroll
+  for (int j = 0; j < RF; ++j) {
+    const int row = 16 * j + x;
+    wp[j] = a.w + ((int64_t)t.g * a.r + (row < a.r ? row : a.r - 1)) * a.k + 8 * q;
+  }
+  v4f sum[RF];
+#pragma unroll
+  for (int j = 0; j < RF; ++j) sum[j] = v4f{0, 0, 0, 0};
+  for (int k0 = w * U * 64; k0 < a.k; k0 += W * U * 64) {
+    v4i zf[U][2], wf[U][2][RF];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = k0 + u * 64 + h * 32;
+        const bool in = at + 8 * q < a.k;
+        zf[u][h] = v4i{0, 0, 0, 0};
+        if (in && pl.tok >= 0) zf[u][h] = load8(zp + at);
+#pragma unroll
+        for (int j = 0; j < RF; ++j) {
+          wf[u][h][j] = v4i{0, 0, 0, 0};
+          if (in) wf[u][h][j] = load8(wp[j] + at);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < RF; ++j) sum[j] = product16<F16>(wf[u][h][j], zf[u][h], sum[j]);
+  }
+  // the weights and the base of the wave's columns are on their way while the sums meet
+  const int c0 = id % p.chunks * (W * 64), n0 = c0 + w * 64;
+  const uint16_t* wg = p.w + (int64_t)t.g * p.r * p.n;
+  v4i base[2], wf[STEPS][4];
+#pragma unroll
+  for (int jp = 0; jp < 2; ++jp) {
+    const int col = n0 + 32 * jp + 8 * q;
+    base[jp] = v4i{0, 0, 0, 0};
+    if (p.base != nullptr && pl.tok >= 0 && col < p.n) base[jp] = load8(p.base + pl.tok * p.n + col);
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = n0 + pair_column(j, x), rank = 16 * s + 8 * (q & 1);
+      wf[s][j] = v4i{0, 0, 0, 0};
+      if (rank < p.r && col < p.n) wf[s][j] = load8(wg + (int64_t)col * p.r + rank);
+    }
+  v4f* part = reinterpret_cast<v4f*>(smem);         // [W][RF][64]
+  float* vs = reinterpret_cast<float*>(smem + W * RF * 1024);      // [16][VP]
+#pragma unroll
+  for (int j = 0; j < RF; ++j) part[(w * RF + j) * 64 + lane] = sum[j];
+  __syncthreads();
+  if (w < RF) {
+    v4f s = part[w * 64 + lane];
+#pragma unroll
+    for (int e = 1; e < W; ++e) s += part[(e * RF + w) * 64 + lane];
+    *reinterpret_cast<v4f*>(vs + x * VP + 16 * w + 4 * q) = s;
+  }
+  __syncthreads();
+  v4f v[STEPS][2];
+  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int rank = 16 * s + 8 * (q & 1);
+    const bool on = pl.tok >= 0 && rank < p.r;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[s][e] = on ? *reinterpret_cast<const v4f*>(vs + x * VP + rank + 4 * e) : v4f{0, 0, 0, 0};
+      if (p.v_out != nullptr && on && c0 == 0 && w == 0 && q < 2)
+        *reinterpret_cast<v4f*>(p.v_out + (int64_t)pl.place * p.r + rank + 4 * e) = v[s][e];
+    }
+  }
+  if constexpr (F16) {
+    pl.largest(v, scale, top);
+    pl.set_factor(top);
+  }
+  pl.split(v, scale);
+  v4f acc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    acc[j] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) acc[j] = product16<F16>(wf[s][j], pl.part[s], acc[j]);
+  }
+#pragma unroll
+  for (int jp = 0; jp < 2; ++jp) {
+    const int col = n0 + 32 * jp + 8 * q;
+    if (pl.tok >= 0 && col < p.n)
+      expand_store<F16>(p.out + pl.tok * p.n + col, base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
+  }
 }
 
 // ------------------------------------------------------------------ outer
@@ -697,24 +921,20 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t tile_bound(int64_t max_rows, int64_t adapters, int64_t bm) {
   return max_rows / bm + (max_rows < adapters ? max_rows : adapters);
 }
-#ifndef XF
-#define XF 512
-#endif
-constexpr int64_t kFill = XF;           // workgroups that fill the chip
+constexpr int64_t kFill = 512;           // workgroups that fill the chip
 
-// Few places an adapter: tiles of 16.  More: of 64, of 128 where those fill the chip.
+// Few places an adapter on average: tiles of 16, more of 64.
 struct ShrinkPlan {
-  int rw, mf, rf, slices;
+  bool many;
+  int rf, slices;
   int64_t tiles;                         // of places
-  bool summed() const { return rw > 1 && slices > 1; }       // by lora_slices; else by the readers
+  bool summed() const { return many && slices > 1 && (slices > 4 || rf == 4); }      // by lora_slices; else by the readers
 };
 ShrinkPlan shrink_plan(int64_t max_rows, int64_t adapters, int64_t k, int64_t r) {
-  ShrinkPlan p{1, 1, r <= 16 ? 1 : r <= 32 ? 2 : 4, 1, 0};
-  if (max_rows > 16 * adapters) p.rw = 4;
-  if (p.rw == 4 && max_rows / 128 >= kFill / 4) p.mf = 2;
-  p.tiles = tile_bound(max_rows, adapters, 16 * p.rw * p.mf);
-  const int64_t wgs = p.tiles * up(r, 16 * p.rf), most = up(k, 64 * kShrinkWaves / p.rw);
-  int64_t s = wgs > 0 ? kFill / wgs : 1;
+  ShrinkPlan p{max_rows > 16 * adapters, r <= 16 ? 1 : r <= 32 ? 2 : 4, 1, 0};
+  p.tiles = tile_bound(max_rows, adapters, p.many ? 64 : 16);
+  const int64_t wgs = p.tiles * up(r, 16 * p.rf), most = up(k, p.many ? 512 : 64 * kShrinkWaves);
+  int64_t s = wgs > 0 ? (p.many && p.rf < 4 ? 2 * kFill : kFill) / wgs : 1;
   s = s < most ? s : most;
   p.slices = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
   return p;
@@ -722,12 +942,9 @@ ShrinkPlan shrink_plan(int64_t max_rows, int64_t adapters, int64_t k, int64_t r)
 // Places of a workgroup: 16 where an adapter has few on average, else 64.
 int expand_places(int64_t max_rows, int64_t adapters) { return max_rows <= 16 * adapters ? 16 : 64; }
 int expand_steps(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
-// Columns of a workgroup: what makes about kFill workgroups, whole 256s.
+// Columns of a workgroup: what makes about 2 kFill workgroups, whole 256s.
 int expand_chunk(int64_t tiles, int64_t n) {
-  #ifndef XE
-#define XE 512
-#endif
-  const int64_t across = tiles > 0 ? up(XE, tiles) : 1;
+    const int64_t across = tiles > 0 ? up(2 * kFill, tiles) : 1;
   return (int)(up(up(n, across), 256) * 256);
 }
 int outer_rf(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
@@ -752,22 +969,24 @@ hipError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&set)[64]) {
   return e;
 }
 
-template <bool F16, bool WT, int RW, int MF, int RF>
-hipError_t shrink_one(hipStream_t s, const ShrinkArgs& p, const ShrinkPlan& plan) {
-  constexpr int kSum = kShrinkWaves * MF * RF * 1024, kW = WT ? kShrinkWaves * 64 * (RF * 32 + 16) : 0;
-  constexpr int bytes = kSum > kW ? kSum : kW;
-  const int64_t wgs = plan.tiles * up(p.r, 16 * RF) * p.slices;
-  static std::atomic<bool> set[64];
-  const hipError_t e = allow_smem(lora_shrink<F16, WT, RW, MF, RF>, bytes, set);
-  if (e != hipSuccess || wgs == 0) return e;
-  hipLaunchKernelGGL((lora_shrink<F16, WT, RW, MF, RF>), dim3((unsigned)wgs), dim3(kShrinkWaves * 64), bytes, s, p);
-  return hipGetLastError();
-}
-template <bool F16, bool WT, int RW, int MF>
+template <bool F16, bool WT, int RF>
 hipError_t shrink_rf(hipStream_t s, const ShrinkArgs& p, const ShrinkPlan& plan) {
-  return plan.rf == 1 ? shrink_one<F16, WT, RW, MF, 1>(s, p, plan)
-         : plan.rf == 2 ? shrink_one<F16, WT, RW, MF, 2>(s, p, plan)
-                        : shrink_one<F16, WT, RW, MF, 4>(s, p, plan);
+  const int64_t wgs = plan.tiles * up(p.r, 16 * RF) * p.slices;
+  if (plan.many) {
+    constexpr int bytes = kManyStages * ShrinkStage<RF>::BYTES;
+    static std::atomic<bool> set[64];
+    const hipError_t e = allow_smem(lora_shrink_many<F16, WT, RF>, bytes, set);
+    if (e != hipSuccess || wgs == 0) return e;
+    hipLaunchKernelGGL((lora_shrink_many<F16, WT, RF>), dim3((unsigned)wgs), dim3(256), bytes, s, p);
+  } else {
+    constexpr int kSum = kShrinkWaves * RF * 1024, kW = WT ? kShrinkWaves * 64 * (RF * 32 + 16) : 0;
+    constexpr int bytes = kSum > kW ? kSum : kW;
+    static std::atomic<bool> set[64];
+    const hipError_t e = allow_smem(lora_shrink_few<F16, WT, RF>, bytes, set);
+    if (e != hipSuccess || wgs == 0) return e;
+    hipLaunchKernelGGL((lora_shrink_few<F16, WT, RF>), dim3((unsigned)wgs), dim3(kShrinkWaves * 64), bytes, s, p);
+  }
+  return hipGetLastError();
 }
 // z w^T into `out` [max_rows, r], or, where the plan leaves the slices to the
 // readers, [slices, max_rows, r]; `parts` holds the slices where they are summed here.
@@ -775,9 +994,9 @@ template <bool F16, bool WT>
 hipError_t shrink(hipStream_t s, const LoraPlan& pl, const uint16_t* z, const uint16_t* w, int64_t k, int64_t r,
                   const ShrinkPlan& plan, float* parts, float* out) {
   const ShrinkArgs p{pl, z, w, plan.summed() ? parts : out, (int)k, (int)r, plan.slices};
-  const hipError_t e = plan.rw == 1   ? shrink_rf<F16, WT, 1, 1>(s, p, plan)
-                       : plan.mf == 1 ? shrink_rf<F16, WT, 4, 1>(s, p, plan)
-                                      : shrink_rf<F16, WT, 4, 2>(s, p, plan);
+  const hipError_t e = plan.rf == 1   ? shrink_rf<F16, WT, 1>(s, p, plan)
+                       : plan.rf == 2 ? shrink_rf<F16, WT, 2>(s, p, plan)
+                                      : shrink_rf<F16, WT, 4>(s, p, plan);
   if (e != hipSuccess || !plan.summed()) return e;
   hipLaunchKernelGGL(lora_slices, dim3((unsigned)up(pl.max_rows * r, 1024)), dim3(256), 0, s, pl, parts, (int)r, plan.slices, out);
   return hipGetLastError();
@@ -815,9 +1034,33 @@ hipError_t expand(hipStream_t s, const ExpandArgs& p) {
   const int steps = expand_steps(p.r);
   return steps == 1 ? expand_steps<F16, WT, 1>(s, p) : steps == 2 ? expand_steps<F16, WT, 2>(s, p) : expand_steps<F16, WT, 4>(s, p);
 }
+// One launch does it: few places an adapter, ranks that a wave's registers hold, and
+// no more workgroups than the chip takes at once (each reads all of its adapter's A).
+bool one_launch(const LoraPlan& pl, int64_t n, int64_t r) {
+  return pl.max_rows <= 16 * pl.adapters && r <= 64 && tile_bound(pl.max_rows, pl.adapters, 16) * up(n, kOneWaves * 64) <= kFill / 2;
+}
+template <bool F16, int STEPS>
+hipError_t one(hipStream_t s, const ShrinkArgs& a, const ExpandArgs& p) {
+  constexpr int bytes = kOneWaves * STEPS * 1024 + 16 * (16 * STEPS + 4) * 4;
+  static std::atomic<bool> set[64];
+  const hipError_t e = allow_smem(lora_one<F16, STEPS>, bytes, set);
+  if (e != hipSuccess || p.tiles + p.rest == 0) return e;
+  hipLaunchKernelGGL((lora_one<F16, STEPS>), dim3(p.tiles + p.rest), dim3(kOneWaves * 64), bytes, s, a, p);
+  return hipGetLastError();
+}
+
 template <bool F16>
 hipError_t forward(hipStream_t s, const LoraArgs& p) {
   const LoraPlan& pl = p.plan;
+  if (one_launch(pl, p.n, p.r)) {
+    const ShrinkArgs a{pl, p.x, p.a, nullptr, (int)p.k, (int)p.r, 1};
+    ExpandArgs x = expand_args(pl, nullptr, p.b, p.base, p.out, p.v, p.n, p.r, 1);
+    x.chunk = kOneWaves * 64;
+    x.chunks = (int)up(p.n, x.chunk);
+    x.tiles = (unsigned)(tile_bound(pl.max_rows, pl.adapters, 16) * x.chunks);
+    const int steps = expand_steps(p.r);
+    return steps == 1 ? one<F16, 1>(s, a, x) : steps == 2 ? one<F16, 2>(s, a, x) : one<F16, 4>(s, a, x);
+  }
   const ShrinkPlan plan = shrink_plan(pl.max_rows, pl.adapters, p.k, p.r);
   // the workspace: the slices (if any), then v where it is not kept
   float* parts = static_cast<float*>(p.workspace);
@@ -890,6 +1133,7 @@ int64_t lora_work_items(int64_t max_rows, int64_t m, int64_t n, int64_t k, int64
     more(most, p.tiles * up(r, 16 * p.rf) * p.slices, kShrinkWaves * 64);
   }
   more(most, up(max_rows * r, 1024), 256);
+  more(most, kFill + up(m, kRestRows) * up(n, kRestCols), kOneWaves * 64);
   for (const int64_t outer : {n, k}) {
     const int64_t wgs = tiles * up(outer, expand_chunk(tiles, outer)) + up(m, kRestRows) * up(outer, kRestCols);
     more(most, wgs, kThreads);
