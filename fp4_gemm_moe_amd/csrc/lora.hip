@@ -305,7 +305,8 @@ __device__ __forceinline__ void expand_rest(const ExpandArgs& p, int id) {
 // .. + 7).  BF16: hi is the value cut to 8 bits, lo the rest rounded.  FP16: a
 // place's values are first scaled by the power of two that takes its largest to
 // [2^14, 2^15), undone in FP32 at the end, so that neither part leaves FP16's range.
-template <bool F16, int STEPS, int SL>
+// SL: slices read at once; HALVES: each half of the wave reads every other slice.
+template <bool F16, int STEPS, int SL, bool HALVES = false>
 struct Places {
   v4i part[STEPS];
   float factor, back;      // the place's power of two, and the one that undoes it
@@ -322,7 +323,8 @@ struct Places {
     const int h = (threadIdx.x >> 4) & 1;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) v[s][0] = v[s][1] = v4f{0, 0, 0, 0};
-    for (int e = 0; e < p.slices; e += SL) {
+    const int each = HALVES ? 2 : 1;
+    for (int e = HALVES ? (threadIdx.x >> 5) & 1 : 0; e < p.slices; e += SL * each) {
       v4f in[SL][STEPS][2];
 #pragma unroll
       for (int i = 0; i < SL; ++i)
@@ -330,8 +332,8 @@ struct Places {
         for (int s = 0; s < STEPS; ++s) {
           in[i][s][0] = in[i][s][1] = v4f{0, 0, 0, 0};
           const int rank = 16 * (s0 + s) + 8 * h;
-          if (tok >= 0 && rank < p.r && e + i < p.slices) {
-            const v4f* src = reinterpret_cast<const v4f*>(p.v + ((int64_t)(e + i) * p.pl.max_rows + place) * p.r + rank);
+          if (tok >= 0 && rank < p.r && e + i * each < p.slices) {
+            const v4f* src = reinterpret_cast<const v4f*>(p.v + ((int64_t)(e + i * each) * p.pl.max_rows + place) * p.r + rank);
             in[i][s][0] = src[0];
             in[i][s][1] = src[1];
           }
@@ -343,6 +345,12 @@ struct Places {
           v[s][0] += in[i][s][0];
           v[s][1] += in[i][s][1];
         }
+    }
+    if constexpr (HALVES) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[s][e >> 2][e & 3] += __shfl_xor(v[s][e >> 2][e & 3], 32, 64);
     }
   }
   // FP16: takes these ranks into the place's largest value
@@ -446,7 +454,7 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& p, int id) {
   const float scale = p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
   uint8_t* wt = smem + w * 16 * STEPS * kFewPitch;
   const uint16_t* wg = p.w + (int64_t)t.g * p.r * p.n;
-  Places<F16, STEPS, STEPS == 4 ? 2 : 4> pl;
+  Places<F16, STEPS, STEPS == 4 ? 2 : 4, true> pl;
   pl.find(p, t, t.row0);
   v4i base[2], wf[STEPS][4];
   auto fetch = [&](int n0, int s0) {
@@ -627,7 +635,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_expand(ExpandArgs p) {
 constexpr int kOneWaves = 16;
 template <bool F16, int STEPS>
 __global__ __launch_bounds__(kOneWaves * 64) void lora_one(ShrinkArgs a, ExpandArgs p) {
-  constexpr int W = kOneWaves, RF = STEPS, U = STEPS == 4 ? 1 : 2, VP = 16 * RF + 4;
+  constexpr int W = kOneWaves, RF = STEPS, U = STEPS == 1 ? 5 : 2, VP = 16 * RF + 4;
   if (blockIdx.x >= p.tiles) {
     if (threadIdx.x < 256) expand_rest(p, (int)(blockIdx.x - p.tiles));
     return;
@@ -656,14 +664,20 @@ __global__ __launch_bounds__(kOneWaves * 64) void lora_one(ShrinkArgs a, ExpandA
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int at = k0 + u * 64 + h * 32;
-        const bool in = at + 8 * q < a.k;
-        zf[u][h] = v4i{0, 0, 0, 0};
-        if (in && pl.tok >= 0) zf[u][h] = load8(zp + at);
 #pragma unroll
         for (int j = 0; j < RF; ++j) {
           wf[u][h][j] = v4i{0, 0, 0, 0};
-          if (in) wf[u][h][j] = load8(wp[j] + at);
+          if (at + 8 * q < a.k) wf[u][h][j] = load8(wp[j] + at);
         }
+      }
+    // after A's, which do not wait for the tokens to be looked up
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = k0 + u * 64 + h * 32;
+        zf[u][h] = v4i{0, 0, 0, 0};
+        if (at + 8 * q < a.k && pl.tok >= 0) zf[u][h] = load8(zp + at);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -737,7 +751,7 @@ __global__ __launch_bounds__(kOneWaves * 64) void lora_one(ShrinkArgs a, ExpandA
 
 // ------------------------------------------------------------------ outer
 // One chunk of an adapter's places: part[chunk] = sum over them of u[place, i]
-// z[token, j], 16 RF ranks i and 128 columns j a workgroup, a wave 32 columns.  64
+// z[token, j], 16 RF ranks i and 256 columns j a workgroup, a wave 64 columns.  32
 // places at a time: z's rows and u, cut into three BF16 parts that hold all its
 // 24 bits, lie in LDS and are read transposed; FP16's z is cut into two BF16
 // parts when it is read, and the products of the least parts (2^-24 of the
@@ -751,7 +765,7 @@ struct OuterArgs {
   int places;              // of a chunk
   unsigned tiles;          // workgroups
 };
-constexpr int kOuterCols = 128, kOuterRows = 64;
+constexpr int kOuterCols = 256, kOuterRows = 32;
 
 template <int RF>
 constexpr int outer_smem() { return kOuterRows * (kOuterCols * 2 + 16) + 3 * kOuterRows * (RF * 32 + 16); }
@@ -769,39 +783,65 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
   const int end = t.row0 + p.places < t.row_end ? t.row0 + p.places : t.row_end;
   uint8_t* zt = smem;
   uint8_t* ut = smem + kOuterRows * ZP;
-  v4f acc[RF][2];
+  v4f acc[RF][4];
 #pragma unroll
-  for (int i = 0; i < RF; ++i) acc[i][0] = acc[i][1] = v4f{0, 0, 0, 0};
-  // a thread's pieces: 16 lanes a row of z (4 pieces), RF * 4 lanes a row of u (RF pieces of four values)
+  for (int i = 0; i < RF; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+  // a thread's pieces: 32 lanes a row of z (4 pieces), 4 RF lanes a row of u (four values each)
+  constexpr int UE = (RF + 1) / 2;
   v4i zr[4];
-  v4f ur[RF];
+  v4f ur[UE];
+  // their places' tokens are looked up a step before
+  int64_t tz[4], tu[UE];
+  auto look = [&](int place0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int place = place0 + (tid >> 5) + 8 * e;
+      tz[e] = place < end ? token_at(p.pl, place) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < UE; ++e) {
+      const int c = tid + 256 * e, place = place0 + c / (4 * RF);
+      tu[e] = c < 128 * RF && place < end ? token_at(p.pl, place) : -1;
+    }
+  };
   auto fetch = [&](int place0) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int place = place0 + (tid >> 4) + 16 * e, col = j0 + (tid & 15) * 8;
-      const int64_t tok = place < end ? token_at(p.pl, place) : -1;
+      const int col = j0 + (tid & 31) * 8;
       zr[e] = v4i{0, 0, 0, 0};
-      if (tok >= 0 && col < p.k) zr[e] = load8(p.z + tok * p.k + col);
+      if (tz[e] >= 0 && col < p.k) zr[e] = load8(p.z + tz[e] * p.k + col);
     }
 #pragma unroll
-    for (int e = 0; e < RF; ++e) {
+    for (int e = 0; e < UE; ++e) {
       const int c = tid + 256 * e, place = place0 + c / (4 * RF), rank = i0 + c % (4 * RF) * 4;
+      const float* src = p.u + (int64_t)place * p.r + rank;
       ur[e] = v4f{0, 0, 0, 0};
-      if (place < end && rank < p.r && token_at(p.pl, place) >= 0) {
-        const float* src = p.u + (int64_t)place * p.r + rank;
-        ur[e] = *reinterpret_cast<const v4f*>(src);
-        for (int s = 1; s < p.slices; ++s) ur[e] += *reinterpret_cast<const v4f*>(src + (int64_t)s * p.pl.max_rows * p.r);
+      for (int s = 0; s < p.slices; s += 4) {
+        v4f in[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          in[i] = v4f{0, 0, 0, 0};
+          if (tu[e] >= 0 && rank < p.r && s + i < p.slices)
+            in[i] = *reinterpret_cast<const v4f*>(src + (int64_t)(s + i) * p.pl.max_rows * p.r);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ur[e] += in[i];
       }
     }
   };
+  look(t.row0);
   fetch(t.row0);
+  look(t.row0 + kOuterRows);
   for (int place0 = t.row0; place0 < end; place0 += kOuterRows) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) *reinterpret_cast<v4i*>(zt + ((tid >> 4) + 16 * e) * ZP + (tid & 15) * 16) = zr[e];
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<v4i*>(zt + ((tid >> 5) + 8 * e) * ZP + (tid & 31) * 16) = zr[e];
 #pragma unroll
-    for (int e = 0; e < RF; ++e) {
+    for (int e = 0; e < UE; ++e) {
       const int c = tid + 256 * e;
+      if (c >= 128 * RF) break;
       uint8_t* d = ut + c / (4 * RF) * UP + c % (4 * RF) * 8;
       float v[4] = {ur[e][0], ur[e][1], ur[e][2], ur[e][3]};
 #pragma unroll
@@ -817,49 +857,47 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
       }
     }
     __syncthreads();
-    if (place0 + kOuterRows < end) fetch(place0 + kOuterRows);
+    if (place0 + kOuterRows < end) {
+      fetch(place0 + kOuterRows);
+      look(place0 + 2 * kOuterRows);
+    }
+    const int row = 8 * q + (x >> 2);
+    v4i uf[RF][3];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = 32 * h + 8 * q + (x >> 2);
-      v4i zf[2][2];
+    for (int i = 0; i < RF; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint8_t* at = zt + row * ZP + (32 * w + 16 * j + 4 * (x & 3)) * 2;
-        zf[j][0] = join(read_transposed(at), read_transposed(at + 4 * ZP));
-        if constexpr (F16) {
-          const v8h v = __builtin_bit_cast(v8h, zf[j][0]);
+      for (int part = 0; part < 3; ++part) {
+        const uint8_t* at = ut + (part * kOuterRows + row) * UP + (16 * i + 4 * (x & 3)) * 2;
+        uf[i][part] = join(read_transposed(at), read_transposed(at + 4 * UP));
+      }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = (float)v[2 * e], b = (float)v[2 * e + 1], ca = bf16_cut(a), cb = bf16_cut(b);
-            uint32_t hi = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u);
-            if (a != a) hi |= 0x7fc0u;
-            if (b != b) hi |= 0x7fc00000u;
-            zf[j][0][e] = (int)hi;
-            zf[j][1][e] = (int)pack_half2<false>(bf16_rest(a, ca), bf16_rest(b, cb));
-          }
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* at = zt + row * ZP + (64 * w + 16 * j + 4 * (x & 3)) * 2;
+      v4i zf = join(read_transposed(at), read_transposed(at + 4 * ZP)), zl = v4i{0, 0, 0, 0};
+      if constexpr (F16) {
+        const v8h v = __builtin_bit_cast(v8h, zf);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = (float)v[2 * e], b = (float)v[2 * e + 1], ca = bf16_cut(a), cb = bf16_cut(b);
+          uint32_t hi = (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u);
+          if (a != a) hi |= 0x7fc0u;
+          if (b != b) hi |= 0x7fc00000u;
+          zf[e] = (int)hi;
+          zl[e] = (int)pack_half2<false>(bf16_rest(a, ca), bf16_rest(b, cb));
         }
       }
 #pragma unroll
       for (int i = 0; i < RF; ++i) {
-        v4i uf[3];
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          const uint8_t* at = ut + (part * kOuterRows + row) * UP + (16 * i + 4 * (x & 3)) * 2;
-          uf[part] = join(read_transposed(at), read_transposed(at + 4 * UP));
+        auto mul = [&](v4i u, v4i z) {
+          acc[i][j] = UT ? product16<false>(u, z, acc[i][j]) : product16<false>(z, u, acc[i][j]);
+        };
+        if constexpr (F16) {
+          mul(uf[i][1], zl);
+          mul(uf[i][0], zl);
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          auto mul = [&](v4i u, v4i z) {
-            acc[i][j] = UT ? product16<false>(u, z, acc[i][j]) : product16<false>(z, u, acc[i][j]);
-          };
-          if constexpr (F16) {
-            mul(uf[1], zf[j][1]);
-            mul(uf[0], zf[j][1]);
-          }
-          mul(uf[2], zf[j][0]);
-          mul(uf[1], zf[j][0]);
-          mul(uf[0], zf[j][0]);
-        }
+        mul(uf[i][2], zf);
+        mul(uf[i][1], zf);
+        mul(uf[i][0], zf);
       }
     }
   }
@@ -868,21 +906,34 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
 #pragma unroll
   for (int i = 0; i < RF; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int rank = i0 + 16 * i + (UT ? 4 * q : x), col = j0 + 32 * w + 16 * j + (UT ? x : 4 * q);
+    for (int j = 0; j < 4; ++j) {
+      const int rank = i0 + 16 * i + (UT ? 4 * q : x), col = j0 + 64 * w + 16 * j + (UT ? x : 4 * q);
       if (rank < p.r && col < p.k)
         *reinterpret_cast<v4f*>(out + (UT ? (int64_t)col * p.r + rank : (int64_t)rank * p.k + col)) = acc[i][j];
     }
 }
 
-// dA's and dB's chunks in one launch.
+// dA's and dB's chunks in one launch; where they are few, dx's tiles too (its
+// registers would keep the chunks from filling the chip).
 struct BackArgs {
   OuterArgs da, db;
+  ExpandArgs dx;
 };
 template <bool F16, int RF>
 __global__ __launch_bounds__(kThreads) void lora_outer(BackArgs p) {
   if (blockIdx.x < p.da.tiles) outer_tile<F16, false, RF>(p.da, (int)blockIdx.x);
   else outer_tile<F16, true, RF>(p.db, (int)(blockIdx.x - p.da.tiles));
+}
+template <bool F16, int RF, bool MANY>
+__global__ __launch_bounds__(kThreads, 2) void lora_back(BackArgs p) {
+  unsigned id = blockIdx.x;
+  if (id < p.da.tiles) return outer_tile<F16, false, RF>(p.da, (int)id);
+  id -= p.da.tiles;
+  if (id < p.db.tiles) return outer_tile<F16, true, RF>(p.db, (int)id);
+  id -= p.db.tiles;
+  if (id >= p.dx.tiles) return expand_rest(p.dx, (int)(id - p.dx.tiles));
+  if constexpr (MANY) expand_many<F16, true, RF>(p.dx, (int)id);
+  else expand_few<F16, true, RF>(p.dx, (int)id);
 }
 
 // da, db: scale times the sum of an adapter's chunks, in order.
@@ -1034,10 +1085,12 @@ hipError_t expand(hipStream_t s, const ExpandArgs& p) {
   const int steps = expand_steps(p.r);
   return steps == 1 ? expand_steps<F16, WT, 1>(s, p) : steps == 2 ? expand_steps<F16, WT, 2>(s, p) : expand_steps<F16, WT, 4>(s, p);
 }
-// One launch does it: few places an adapter, ranks that a wave's registers hold, and
-// no more workgroups than the chip takes at once (each reads all of its adapter's A).
-bool one_launch(const LoraPlan& pl, int64_t n, int64_t r) {
-  return pl.max_rows <= 16 * pl.adapters && r <= 64 && tile_bound(pl.max_rows, pl.adapters, 16) * up(n, kOneWaves * 64) <= kFill / 2;
+// One launch does it: few places an adapter, ranks that a wave's registers hold,
+// no more workgroups than the chip takes at once, and an A that one compute unit
+// reads in about a launch's time (every workgroup reads all of its adapter's).
+bool one_launch(const LoraPlan& pl, int64_t n, int64_t k, int64_t r) {
+  return pl.max_rows <= 16 * pl.adapters && r <= 64 && r * k <= 3 << 15 &&
+         tile_bound(pl.max_rows, pl.adapters, 16) * up(n, kOneWaves * 64) <= kFill / 2;
 }
 template <bool F16, int STEPS>
 hipError_t one(hipStream_t s, const ShrinkArgs& a, const ExpandArgs& p) {
@@ -1052,7 +1105,7 @@ hipError_t one(hipStream_t s, const ShrinkArgs& a, const ExpandArgs& p) {
 template <bool F16>
 hipError_t forward(hipStream_t s, const LoraArgs& p) {
   const LoraPlan& pl = p.plan;
-  if (one_launch(pl, p.n, p.r)) {
+  if (one_launch(pl, p.n, p.k, p.r)) {
     const ShrinkArgs a{pl, p.x, p.a, nullptr, (int)p.k, (int)p.r, 1};
     ExpandArgs x = expand_args(pl, nullptr, p.b, p.base, p.out, p.v, p.n, p.r, 1);
     x.chunk = kOneWaves * 64;
@@ -1087,6 +1140,23 @@ hipError_t outer(hipStream_t s, const BackArgs& p) {
   hipLaunchKernelGGL((lora_outer<F16, RF>), dim3(wgs), dim3(kThreads), outer_smem<RF>(), s, p);
   return hipGetLastError();
 }
+template <bool F16, int RF, bool MANY>
+hipError_t back_one(hipStream_t s, const BackArgs& p) {
+  constexpr int a = MANY ? 2 * ManyCfg<true, RF>::BUF : 4 * 16 * RF * kFewPitch, b = outer_smem<RF>(), bytes = a > b ? a : b;
+  static std::atomic<bool> set[64];
+  const hipError_t e = allow_smem(lora_back<F16, RF, MANY>, bytes, set);
+  const unsigned wgs = p.da.tiles + p.db.tiles + p.dx.tiles + p.dx.rest;
+  if (e != hipSuccess || wgs == 0) return e;
+  hipLaunchKernelGGL((lora_back<F16, RF, MANY>), dim3(wgs), dim3(kThreads), bytes, s, p);
+  return hipGetLastError();
+}
+template <bool F16, int RF>
+hipError_t back(hipStream_t s, const BackArgs& p, const LoraPlan& pl) {
+  if (p.dx.out != nullptr && (int64_t)p.da.tiles + p.db.tiles + p.dx.tiles <= 2 * kFill)
+    return expand_places(pl.max_rows, pl.adapters) == 16 ? back_one<F16, RF, false>(s, p) : back_one<F16, RF, true>(s, p);
+  const hipError_t e = outer<F16, RF>(s, p);
+  return e != hipSuccess || p.dx.out == nullptr ? e : expand<F16, true>(s, p.dx);
+}
 
 template <bool F16>
 hipError_t backward(hipStream_t s, const LoraArgs& p) {
@@ -1105,13 +1175,10 @@ hipError_t backward(hipStream_t s, const LoraArgs& p) {
   BackArgs x;
   x.da = OuterArgs{pl, u, p.x, pa, (int)p.k, (int)p.r, slices, places, (unsigned)(each * up(p.k, kOuterCols))};
   x.db = OuterArgs{pl, p.v, p.dy, pb, (int)p.n, (int)p.r, 1, places, (unsigned)(each * up(p.n, kOuterCols))};
+  x.dx = expand_args(pl, u, p.a, p.base, p.out, nullptr, p.k, p.r, slices);
   const int rf = outer_rf(p.r);
-  e = rf == 1 ? outer<F16, 1>(s, x) : rf == 2 ? outer<F16, 2>(s, x) : outer<F16, 4>(s, x);
+  e = rf == 1 ? back<F16, 1>(s, x, pl) : rf == 2 ? back<F16, 2>(s, x, pl) : back<F16, 4>(s, x, pl);
   if (e != hipSuccess) return e;
-  if (p.out != nullptr) {
-    e = expand<F16, true>(s, expand_args(pl, u, p.a, p.base, p.out, nullptr, p.k, p.r, slices));
-    if (e != hipSuccess) return e;
-  }
   SumArgs m{pl, pa, pb, p.da, p.db, p.r * p.k, p.r * p.n, places, (unsigned)up(p.r * (p.k + p.n), 4 * kThreads), p.accumulate};
   hipLaunchKernelGGL(lora_sum, dim3(m.blocks * (unsigned)pl.adapters), dim3(kThreads), 0, s, m);
   return hipGetLastError();
