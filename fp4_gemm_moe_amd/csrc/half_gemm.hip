@@ -92,6 +92,14 @@ constexpr int kDirect = -1;      // not a tile: the direct kernel
 //    256x256 one: T = 512 229 (128x128), 284 (256x256), T = 1024 300, 303, T = 2048
 //    424, 398; slots of 128 rows 119, 138; sums over the groups' rows, 8 groups of
 //    128 rows, 1024 x 768: 13.6, 17.4; 64 of 256 rows, 2048 x 1536: 317, 260.
+// Results that the L2s cannot hold leave past them, and the operands stay: 65536
+// rows x 4096 688 -> 685 us, their sums for the weights (805 MB) 737 -> 722 us, 402 MB
+// of such sums 215 -> 219 us.
+bool plan_stream(const HalfGemmArgs& p) {
+  const int64_t bytes = (p.form == kGroupK ? p.groups : 1) * p.rows * p.n * (p.out_kind >= kOutF32 ? 4 : 2);
+  return bytes > (int64_t)32 << 20;
+}
+
 int plan_half(const HalfGemmArgs& p, const DeviceInfo& dev) {
   const int64_t cus = dev.num_cus;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
@@ -112,7 +120,9 @@ int plan_half(const HalfGemmArgs& p, const DeviceInfo& dev) {
 
 }  // namespace
 
-hipError_t launch_half_gemm(hipStream_t s, const HalfGemmArgs& p, const DeviceInfo& dev) {
+hipError_t launch_half_gemm(hipStream_t s, const HalfGemmArgs& args, const DeviceInfo& dev) {
+  HalfGemmArgs p = args;
+  p.stream = plan_stream(p);
   const int tile = plan_half(p, dev);
   if (p.form == kGroupK) return launch_half_tn(s, p, dev, tile);
   if (tile == kDirect) return launch_direct(s, p, direct_tiles(p));

@@ -22,6 +22,7 @@ struct HalfGemmArgs {
   int32_t form;
   int32_t out_kind;          // BlockOut
   bool b_t, f16;
+  bool stream;               // tiled kernel: results leave past the caches
 };
 hipError_t launch_half_gemm(hipStream_t s, const HalfGemmArgs& args, const DeviceInfo& dev);
 

@@ -59,8 +59,9 @@ struct Cfg {
 
 struct Table {
   int end[kMaxGroups];     // rows where group g ends
-  int tiles[kMaxGroups];   // inclusive count of m-tiles (row forms)
+  int tiles[kMaxGroups];   // row forms: inclusive count of m-tiles; else: the groups, longest first
 };
+constexpr int kSortedGroups = 128;
 
 // Where a tile sits (uniform).
 struct Tile {
@@ -141,6 +142,20 @@ __global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p)
   if constexpr (AT) {
     load_clamped_ends<C::THREADS>(table.end, p.group_end, p.groups, p.k);
     mt_total = (int)((p.rows + C::BM - 1) / C::BM);
+    // Workgroups take whole rounds of tiles, a group's after the other's: with the
+    // longest first the rounds at the end, where they differ, are the short ones
+    // (more groups than kSortedGroups come as they are: the search is quadratic).
+    for (int g = tid; g < p.groups; g += C::THREADS) {
+      int rank = g;
+      if (p.groups <= kSortedGroups) {
+        auto len = [&](int i) { return table.end[i] - (i > 0 ? table.end[i - 1] : 0); };
+        const int mine = len(g);
+        rank = 0;
+        for (int i = 0; i < p.groups; ++i) rank += len(i) > mine || (len(i) == mine && i < g);
+      }
+      table.tiles[rank] = g;
+    }
+    __syncthreads();
   } else {
     if (p.form == kContiguous) {
       load_clamped_ends<C::THREADS>(table.end, p.group_end, p.groups, p.rows);
@@ -196,7 +211,7 @@ __global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p)
       t.n0 = (int64_t)ni * C::BN;
       const int64_t nn = p.n - t.n0 < C::BN ? p.n - t.n0 : C::BN;
       if constexpr (AT) {
-        t.g = outer;
+        t.g = (int)ufirst((uint32_t)table.tiles[outer]);
         t.row0 = (int64_t)mt * C::BM;
         t.row_end = p.rows;
         const int64_t k0 = (int)ufirst((uint32_t)(t.g > 0 ? table.end[t.g - 1] : 0));
@@ -360,6 +375,10 @@ __global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p)
 #pragma unroll
   for (int r = 0; r < R; ++r) read1(r, 0);
 
+  // the fewest stores of a tile, on top of the loads that may be under way
+  constexpr int kStores = FI * 16 * C::WTN * 2 / 1024, kMost = (ST - 2) * kOps + BL + kStores;
+  constexpr int kStoreWait = kMost < 63 ? kMost : 63;
+  bool stored = false;
   for (int round = 0; tile_at(round) < total; ++round) {
     Tile t;
     {
@@ -379,7 +398,10 @@ __global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p)
       half(std::integral_constant<int, 0>(), stage, stage);
       // this wave has read its stage, and the next step's has landed
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      wait_vm<(ST - 2) * kOps + BL>();
+      // after a tile's stores, these may be under way too
+      if (stored) wait_vm<kStoreWait>();
+      else wait_vm<(ST - 2) * kOps + BL>();
+      stored = false;
       bar();
       const uint32_t freed = stage;
       stage = next_stage();
@@ -393,9 +415,14 @@ __global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p)
     // whole lines: lane (x, q) holds columns 16 j + 4 q .. + 3 of row x.
     const int x = lane & 15, q = lane >> 4;
     uint8_t* mine = smem + ST * C::STAGE + w * C::ESHARE;
-    const int64_t wrow0 = t.row0 + wm * C::WTM, wn0 = t.n0 + wn * C::WTN;
     const int64_t orow = AT ? (int64_t)t.g * p.rows : 0;
-    auto store = [&](auto esc, auto addc) {
+    // Stores past the tile's rows or the output's columns are dropped by the
+    // buffer's end, not branched around: their number is known to the next wait.
+    const uint32_t es = p.out_kind >= kOutF32 ? 4 : 2, opitch = (uint32_t)p.n * es;
+    const int64_t rows = t.row_end - t.row0 < C::BM ? t.row_end - t.row0 : C::BM;
+    const uint8_t* o0 = uniform(static_cast<const uint8_t*>(p.out) + ((orow + t.row0) * p.n + t.n0) * es);
+    const __amdgpu_buffer_rsrc_t dst = rsrc(o0, ufirst((uint32_t)(rows * opitch - t.n0 * es)));
+    auto store = [&](auto esc, auto addc, auto ntc) {
       constexpr int ES = decltype(esc)::value;
       constexpr int COLS = C::EROW / ES, PARTS = C::WTN / COLS, FP = FJ / PARTS;      // columns and fragments at a time
       constexpr int CH = C::EROW / 16, RPI = 64 / CH;                             // rows a store instruction
@@ -413,24 +440,29 @@ __global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p)
             else *reinterpret_cast<v4f*>(d) = v;
           }
           fence();
-          const int64_t n = wn0 + part * COLS + ch * (16 / ES);
+          const int n = wn * C::WTN + part * COLS + ch * (16 / ES);
+          const uint32_t off = (uint32_t)(wm * C::WTM + 16 * i + lrow) * opitch + (uint32_t)n * ES | (t.n0 + n < p.n ? 0u : 0x80000000u);
 #pragma unroll
           for (int r = 0; r < 16 / RPI; ++r) {
             v4f v = *reinterpret_cast<const v4f*>(mine + (r * RPI + lrow) * C::ESTRIDE + ch * 16);
-            const int64_t row = wrow0 + 16 * i + r * RPI + lrow;
-            if (row < t.row_end && n < p.n) {
-              v4f* d = reinterpret_cast<v4f*>(static_cast<uint8_t*>(p.out) + ((orow + row) * p.n + n) * ES);
-              if constexpr (decltype(addc)::value) v = *d + v;
-              *d = v;
-            }
+            const uint32_t at = off + (uint32_t)(r * RPI) * opitch;
+            typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+            if constexpr (decltype(addc)::value)
+              v += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(dst, (int)at, 0, 0));
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), dst, (int)at, 0, decltype(ntc)::value ? 2 : 0);
           }
           fence();
         }
       }
     };
-    if (p.out_kind == kOutF32) store(std::integral_constant<int, 4>(), std::false_type());
-    else if (p.out_kind == kOutF32Add) store(std::integral_constant<int, 4>(), std::true_type());
-    else store(std::integral_constant<int, 2>(), std::false_type());
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    if (p.out_kind == kOutF32Add) store(std::integral_constant<int, 4>(), yes, no);
+    else if (p.out_kind == kOutF32 && p.stream) store(std::integral_constant<int, 4>(), no, yes);
+    else if (p.out_kind == kOutF32) store(std::integral_constant<int, 4>(), no, no);
+    else if (p.stream) store(std::integral_constant<int, 2>(), no, yes);
+    else store(std::integral_constant<int, 2>(), no, no);
+    stored = true;
   }
   wait_vm<0>();       // no load may land in LDS after the workgroup has ended
 }
