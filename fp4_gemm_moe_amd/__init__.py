@@ -824,40 +824,43 @@ def moe_sort(topk_ids, num_experts, align=1):
 
 
 # ---------------------------------------------------------------- 16-bit products by expert
-class _Call:
-    """One call's tensors: their addresses, checked like _arg's, all of one device.
-    Entered, it makes that device the current one, which the library launches on."""
+def _device(t):
+    """The device number of a call's first tensor: all of them have to be there."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("tensors must be device tensors")
+    return d
 
-    def __init__(self, first):
-        self.device = first.get_device()
-        if self.device < 0:
-            raise ValueError("tensors must be device tensors")
 
-    def arg(self, t, name, dtype, shape):
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device or not t.is_contiguous():
-            _need(t, name, dtype)
-            if t.get_device() != self.device:
-                raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors on cuda:{self.device}")
-            raise ValueError(f"{name} has the shape {tuple(t.shape)}, expected {tuple(shape)}")
-        return t.data_ptr()
+def _at(t, name, dtype, shape, device):
+    """The address of a contiguous tensor of this dtype and shape on this device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _need(t, name, dtype)
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors on cuda:{device}")
+        raise ValueError(f"{name} has the shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
 
-    def opt(self, t, name, dtype, shape):
-        return None if t is None else self.arg(t, name, dtype, shape)
 
-    def workspace(self, t):
-        if t is None:
-            return None, 0
-        if t.get_device() != self.device or not t.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
-        return t.data_ptr(), t.numel() * t.element_size()
+def _space(t, device):
+    """A workspace's address and bytes."""
+    if t is None:
+        return None, 0
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
-    def run(self, fn, *args):
-        """fn(the device's current stream, *args)."""
-        if self.device == torch.cuda.current_device():
-            _check(fn(torch._C._cuda_getCurrentRawStream(self.device), *args))
-        else:
-            with torch.cuda.device(self.device):
-                _check(fn(torch._C._cuda_getCurrentRawStream(self.device), *args))
+
+def _run(device, fn, *args):
+    """fn(the device's current stream, *args) with that device as the current one,
+    which the library launches on."""
+    if device == torch._C._cuda_getDevice():
+        status = fn(torch._C._cuda_getCurrentRawStream(device), *args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(torch._C._cuda_getCurrentRawStream(device), *args)
+    if status:
+        raise HQError(status, hq_last_error())
 
 
 def _half_dtype(t, name):
@@ -883,45 +886,49 @@ def hq_half_group_contiguous_gemm(a, b, group_end, out, transpose=False, accumul
     float32 (accumulate: out += the product).  With transpose b is [E, k, n] and
     out[r] = a[r] b[g]: the gradient for the activations.  Rows past the last end
     are left alone."""
-    c = _Call(a)
+    d = _device(a)
     dt, flags = _half_product(a, out, transpose, accumulate)
     rows, k = a.shape
     E, n = b.shape[0], b.shape[2 if transpose else 1]
-    c.run(load().hq_half_group_contiguous_gemm, flags, c.arg(a, "a", dt, (rows, k)),
-          c.arg(b, "b", dt, (E, k, n) if transpose else (E, n, k)), c.arg(group_end, "group_end", torch.int32, (E,)), E,
-          c.arg(out, "out", out.dtype, (rows, n)), rows, n, k)
+    _run(d, load().hq_half_group_contiguous_gemm, flags, _at(a, "a", dt, (rows, k), d),
+         _at(b, "b", dt, (E, k, n) if transpose else (E, n, k), d), _at(group_end, "group_end", torch.int32, (E,), d),
+         E, _at(out, "out", out.dtype, (rows, n), d), rows, n, k)
 
 
 def hq_half_group_masked_gemm(a, b, masked_m, out, max_m, transpose=False, accumulate=False):
     """The same for expert e's first masked_m[e] rows of slot [e*max_m, (e+1)*max_m)."""
-    c = _Call(a)
+    d = _device(a)
     dt, flags = _half_product(a, out, transpose, accumulate)
     rows, k = a.shape
     E, n = b.shape[0], b.shape[2 if transpose else 1]
     if rows != E * max_m:
         raise ValueError(f"a has {rows} rows, expected num_groups * max_m = {E * max_m}")
-    c.run(load().hq_half_group_masked_gemm, flags, c.arg(a, "a", dt, (rows, k)),
-          c.arg(b, "b", dt, (E, k, n) if transpose else (E, n, k)), c.arg(masked_m, "masked_m", torch.int32, (E,)), E,
-          max_m, c.arg(out, "out", out.dtype, (rows, n)), n, k)
+    _run(d, load().hq_half_group_masked_gemm, flags, _at(a, "a", dt, (rows, k), d),
+         _at(b, "b", dt, (E, k, n) if transpose else (E, n, k), d), _at(masked_m, "masked_m", torch.int32, (E,), d), E,
+         max_m, _at(out, "out", out.dtype, (rows, n), d), n, k)
 
 
 def hq_half_group_k_gemm(a, b, group_end, out, accumulate=False):
     """out[g] = sum over the rows r in [group_end[g-1], group_end[g]) of a[r]^T b[r]:
     a [rows, m] and b [rows, n] bfloat16 or float16, out [E, m, n] of that type or
     float32 -- the gradient for the weights, from a product's operands as they are."""
-    c = _Call(a)
+    d = _device(a)
     dt, flags = _half_product(a, out, False, accumulate)
     rows, m = a.shape
     n, E = b.shape[1], group_end.numel()
-    c.run(load().hq_half_group_k_gemm, flags, c.arg(a, "a", dt, (rows, m)), c.arg(b, "b", dt, (rows, n)),
-          c.arg(group_end, "group_end", torch.int32, (E,)), E, c.arg(out, "out", out.dtype, (E, m, n)), m, n, rows)
+    _run(d, load().hq_half_group_k_gemm, flags, _at(a, "a", dt, (rows, m), d), _at(b, "b", dt, (rows, n), d),
+         _at(group_end, "group_end", torch.int32, (E,), d), E, _at(out, "out", out.dtype, (E, m, n), d), m, n, rows)
 
 
-def _selection(c, rows, num_groups, group_end, slot_rows, valid):
+def _selection(d, rows, num_groups, group_end, slot_rows, valid):
     if group_end is not None and num_groups == 0:
         num_groups = group_end.numel()
-    return (num_groups, c.opt(group_end, "group_end", torch.int32, (num_groups,)), slot_rows,
-            c.opt(valid, "valid", torch.int32, (num_groups,)))
+    if num_groups == 0:
+        if group_end is not None or valid is not None:         # an empty one's address is NULL: all rows
+            raise ValueError("group_end and valid need at least one group")
+        return 0, None, slot_rows, None
+    return (num_groups, None if group_end is None else _at(group_end, "group_end", torch.int32, (num_groups,), d),
+            slot_rows, None if valid is None else _at(valid, "valid", torch.int32, (num_groups,), d))
 
 
 def hq_swiglu(x, y, num_groups=0, group_end=None, slot_rows=0, valid=None):
@@ -929,22 +936,23 @@ def hq_swiglu(x, y, num_groups=0, group_end=None, slot_rows=0, valid=None):
     bfloat16 or float16.  All rows, or by group as in hq_fused_swiglu_quant: those
     up to group_end [num_groups], or slots of slot_rows, and of each group the first
     valid[g].  Other rows are left alone."""
-    c = _Call(x)
+    d = _device(x)
     dt = _half_dtype(x, "x")
     rows, h = x.shape[0], x.shape[1] // 2
-    sel = _selection(c, rows, num_groups, group_end, slot_rows, valid)
-    c.run(load().hq_swiglu, c.arg(x, "x", dt, (rows, 2 * h)), rows, h, *sel, c.arg(y, "y", dt, (rows, h)), _in_flag(x))
+    sel = _selection(d, rows, num_groups, group_end, slot_rows, valid)
+    _run(d, load().hq_swiglu, _at(x, "x", dt, (rows, 2 * h), d), rows, h, *sel, _at(y, "y", dt, (rows, h), d),
+         _in_flag(x))
 
 
 def hq_swiglu_backward(dy, x, dx, y=None, num_groups=0, group_end=None, slot_rows=0, valid=None):
     """The gradient dx [rows, 2h] of hq_swiglu for dy [rows, h], and y once more
     where it is given.  dx may be x, and y may be dy."""
-    c = _Call(x)
+    d = _device(x)
     dt = _half_dtype(x, "x")
     rows, h = x.shape[0], x.shape[1] // 2
-    sel = _selection(c, rows, num_groups, group_end, slot_rows, valid)
-    c.run(load().hq_swiglu_backward, c.arg(dy, "dy", dt, (rows, h)), c.arg(x, "x", dt, (rows, 2 * h)), rows, h, *sel,
-          c.arg(dx, "dx", dt, (rows, 2 * h)), c.opt(y, "y", dt, (rows, h)), _in_flag(x))
+    sel = _selection(d, rows, num_groups, group_end, slot_rows, valid)
+    _run(d, load().hq_swiglu_backward, _at(dy, "dy", dt, (rows, h), d), _at(x, "x", dt, (rows, 2 * h), d), rows, h,
+         *sel, _at(dx, "dx", dt, (rows, 2 * h), d), None if y is None else _at(y, "y", dt, (rows, h), d), _in_flag(x))
 
 
 # ---------------------------------------------------------------- low-rank adapters
@@ -964,7 +972,7 @@ def hq_lora_backward_workspace_size(m, n, k, r, adapters, max_rows=None):
     return _lora_size(load().hq_lora_backward_workspace_size, m, n, k, r, adapters, max_rows)
 
 
-def _lora_plan(c, m, L, row_map, row_pair):
+def _lora_plan(d, m, L, row_map, row_pair):
     if (row_map is None) != (row_pair is None):
         raise ValueError("row_map and row_pair go together")
     if row_pair is None:
@@ -972,7 +980,7 @@ def _lora_plan(c, m, L, row_map, row_pair):
     places = row_pair.numel()
     if row_map.dim() == 2:                     # as hq_moe_sort has it, with topk 1
         row_map = row_map[:, 0]
-    return c.arg(row_map, "row_map", torch.int32, (m,)), c.arg(row_pair, "row_pair", torch.int32, (places,)), places
+    return _at(row_map, "row_map", torch.int32, (m,), d), _at(row_pair, "row_pair", torch.int32, (places,), d), places
 
 
 def hq_lora(x, a, b, scale, group_end, out, base=None, row_map=None, row_pair=None, v=None, workspace=None):
@@ -983,17 +991,19 @@ def hq_lora(x, a, b, scale, group_end, out, base=None, row_map=None, row_pair=No
     in the order of their adapters.  Tokens without an adapter get base's rows
     (zeros without a base, and are left alone where base is out).  v float32
     [places, r] keeps x a^T for the gradients."""
-    c = _Call(x)
+    d = _device(x)
     dt = _half_dtype(x, "x")
     m, k = x.shape
     L, r = a.shape[:2]
     n = b.shape[1]
-    mp, pp, places = _lora_plan(c, m, L, row_map, row_pair)
-    wp, wb = c.workspace(workspace)
-    c.run(load().hq_lora, _in_flag(x), c.arg(x, "x", dt, (m, k)), c.arg(a, "a", dt, (L, r, k)),
-          c.arg(b, "b", dt, (L, n, r)), c.opt(scale, "scale", torch.float32, (L,)),
-          c.arg(group_end, "group_end", torch.int32, (L,)), L, mp, pp, places, c.opt(base, "base", dt, (m, n)),
-          c.arg(out, "out", dt, (m, n)), c.opt(v, "v", torch.float32, (places, r)), m, n, k, r, wp, wb)
+    mp, pp, places = _lora_plan(d, m, L, row_map, row_pair)
+    wp, wb = _space(workspace, d)
+    _run(d, load().hq_lora, _in_flag(x), _at(x, "x", dt, (m, k), d), _at(a, "a", dt, (L, r, k), d),
+         _at(b, "b", dt, (L, n, r), d), None if scale is None else _at(scale, "scale", torch.float32, (L,), d),
+         _at(group_end, "group_end", torch.int32, (L,), d), L, mp, pp, places,
+         None if base is None else _at(base, "base", dt, (m, n), d),
+         _at(out, "out", dt, (m, n), d), None if v is None else _at(v, "v", torch.float32, (places, r), d),
+         m, n, k, r, wp, wb)
 
 
 def hq_lora_backward(dy, x, v, a, b, scale, group_end, da, db, dx=None, base=None, row_map=None, row_pair=None,
@@ -1001,19 +1011,20 @@ def hq_lora_backward(dy, x, v, a, b, scale, group_end, da, db, dx=None, base=Non
     """The gradients of hq_lora for dy [m, n]: dx [m, k] = base + the adapters' share
     (base: the gradient for x through the projection; dx None: not computed), da
     float32 [L, r, k] and db float32 [L, n, r] (accumulate: added to them)."""
-    c = _Call(x)
+    d = _device(x)
     dt = _half_dtype(x, "x")
     m, k = x.shape
     L, r = a.shape[:2]
     n = b.shape[1]
-    mp, pp, places = _lora_plan(c, m, L, row_map, row_pair)
-    wp, wb = c.workspace(workspace)
-    c.run(load().hq_lora_backward, _in_flag(x) | (HQ_ACCUMULATE if accumulate else 0), c.arg(dy, "dy", dt, (m, n)),
-          c.arg(x, "x", dt, (m, k)), c.arg(v, "v", torch.float32, (places, r)), c.arg(a, "a", dt, (L, r, k)),
-          c.arg(b, "b", dt, (L, n, r)), c.opt(scale, "scale", torch.float32, (L,)),
-          c.arg(group_end, "group_end", torch.int32, (L,)), L, mp, pp, places, c.opt(base, "base", dt, (m, k)),
-          c.opt(dx, "dx", dt, (m, k)), c.arg(da, "da", torch.float32, (L, r, k)),
-          c.arg(db, "db", torch.float32, (L, n, r)), m, n, k, r, wp, wb)
+    mp, pp, places = _lora_plan(d, m, L, row_map, row_pair)
+    wp, wb = _space(workspace, d)
+    _run(d, load().hq_lora_backward, _in_flag(x) | (HQ_ACCUMULATE if accumulate else 0), _at(dy, "dy", dt, (m, n), d),
+         _at(x, "x", dt, (m, k), d), _at(v, "v", torch.float32, (places, r), d), _at(a, "a", dt, (L, r, k), d),
+         _at(b, "b", dt, (L, n, r), d), None if scale is None else _at(scale, "scale", torch.float32, (L,), d),
+         _at(group_end, "group_end", torch.int32, (L,), d), L, mp, pp, places,
+         None if base is None else _at(base, "base", dt, (m, k), d),
+         None if dx is None else _at(dx, "dx", dt, (m, k), d), _at(da, "da", torch.float32, (L, r, k), d),
+         _at(db, "db", torch.float32, (L, n, r), d), m, n, k, r, wp, wb)
 
 
 def lora_plan(adapter_ids, num_adapters):
