@@ -61,7 +61,6 @@ class MoeBlockFp8:
         x, weights, row_map, ends, counts, gu, y = saved
         dev, h, m, E = dout.device, self.hidden, self.inter, self.experts
         rows = y.shape[0]
-        used = torch.arange(rows, device=dev)[:, None] < ends[-1]      # rows past the last group hold anything
         dy = torch.empty_like(y)
         dweights = torch.empty_like(weights)
         hq.hq_moe_combine_backward(dout, y, row_map, weights, ends, counts, dy, dweights)
@@ -69,11 +68,8 @@ class MoeBlockFp8:
         da = torch.empty((rows, m), dtype=torch.bfloat16, device=dev)
         hq.hq_block_group_contiguous_gemm(*hq.block_quantize(dy), *self.w2_t, ends, da)
         # through SwiGLU, a = up * silu(gate)
-        gate, up = torch.where(used, gu, 0).float().split(m, 1)
-        s = torch.sigmoid(gate)
-        a = (up * gate * s).bfloat16()
-        g = torch.where(used, da, 0).float()
-        dgu = torch.cat([g * up * s * (1 + gate * (1 - s)), g * gate * s], 1).bfloat16()
+        dgu, a = torch.empty_like(gu), torch.empty_like(da)
+        hq.hq_swiglu_backward(da, gu, dgu, y=a, group_end=ends)
         # through the gate|up product, and back into tokens
         dxr = torch.empty((rows, h), dtype=torch.bfloat16, device=dev)
         hq.hq_block_group_contiguous_gemm(*hq.block_quantize(dgu), *self.w1_t, ends, dxr)
