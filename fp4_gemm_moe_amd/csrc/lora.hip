@@ -995,7 +995,7 @@ int expand_places(int64_t max_rows, int64_t adapters) { return max_rows <= 16 * 
 int expand_steps(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 // Columns of a workgroup: what makes about 2 kFill workgroups, whole 256s.
 int expand_chunk(int64_t tiles, int64_t n) {
-    const int64_t across = tiles > 0 ? up(2 * kFill, tiles) : 1;
+  const int64_t across = tiles > 0 ? up(2 * kFill, tiles) : 1;
   return (int)(up(up(n, across), 256) * 256);
 }
 int outer_rf(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }

@@ -714,9 +714,11 @@ hq_status hq_swiglu_backward(void* stream, const uint16_t* dy, const uint16_t* x
  * Sums are FP32; x A^T keeps FP32, and the product with B takes it to at least
  * 16 bits (of each value, for BF16; of the largest in the token's row, for
  * FP16); out is rounded once.  An adapter of a smaller rank holds zeros in the
- * rest of its rows of A or columns of B.
+ * rest of its rows of A or columns of B.  Values that are not finite stay with
+ * their tokens and adapters; an infinity may come out as NaN.
  * base NULL counts as zeros.  Tokens without an adapter get base's row (zeros
- * without base); where base is out, they are not touched.
+ * without base); where base is out, they are not touched.  No other operand may
+ * overlap a result.
  *
  * The plan is hq_moe_sort's with topk 1 and the tokens' adapters as ids (-1, or
  * any other id outside [0, num_adapters), for none), made once for all layers of

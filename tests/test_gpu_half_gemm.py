@@ -41,6 +41,8 @@ CONTIG = [
     ([64, 64], 0, 128, 72), ([300], 1, 520, 200), ([257, 1, 513, 0, 130], 70, 256, 320),
     ([17] * 40, 0, 96, 512), ([1] * 7 + [0] * 9, 1, 1536, 2048), ([700, 900], 0, 776, 1032), ([130, 600, 20], 9, 4096, 64),
     ([2600, 3100], 33, 520, 192), ([1200] * 4 + [5], 0, 384, 96),
+    # results of more than 32 MB: many tiles a workgroup, of one step each and of some
+    ([2100, 3, 2101], 7, 4104, 64), ([4300, 1200], 0, 4096, 200), ([20] * 200, 0, 2056, 40),
 ]
 
 
@@ -76,7 +78,8 @@ def test_contiguous_clamps_ends(ends, transpose):
     _check_rows(what, whole, out, ref, mag, 64)
 
 
-@pytest.mark.parametrize("sizes,n,k", [([5, 0, 90], 72, 104), ([700, 300], 264, 520), ([1, 2, 0, 1], 520, 264)])
+@pytest.mark.parametrize("sizes,n,k", [([5, 0, 90], 72, 104), ([700, 300], 264, 520), ([1, 2, 0, 1], 520, 264),
+                                       ([2000, 2300], 2056, 72)])
 @pytest.mark.parametrize("transpose", [False, True])
 def test_contiguous_accumulates(sizes, n, k, transpose):
     what = f"contiguous accumulate {sizes} n={n} k={k} t={transpose}"
@@ -109,7 +112,8 @@ def test_more_groups_than_rows():
 
 @pytest.mark.parametrize("counts,max_m,n,k", [
     ([1, 0, 3], 3, 64, 72), ([16, -4, 99, 7], 16, 136, 264), ([64, 0, 33, 1, 63], 64, 264, 520),
-    ([130, 5, 0, 128], 130, 256, 128), ([300, 0, 1], 300, 520, 192), ([0, 0], 5, 16, 16), ([9] * 70, 20, 200, 64)])
+    ([130, 5, 0, 128], 130, 256, 128), ([300, 0, 1], 300, 520, 192), ([0, 0], 5, 16, 16), ([9] * 70, 20, 200, 64),
+    ([64, 3, 50, 0] * 16, 64, 4104, 72), ([30, 31] * 40, 32, 2056, 136), ([8] * 64, 8, 4104, 1032)])
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (F16, F32)])
 def test_masked(counts, max_m, n, k, transpose, dtype, out_dtype):
@@ -130,7 +134,8 @@ def test_masked(counts, max_m, n, k, transpose, dtype, out_dtype):
 # (sizes, rows past the last end, m, n)
 KGROUP = [([1], 0, 8, 8), ([0, 5, 33, 0], 3, 16, 40), ([64, 1, 127, 31], 0, 72, 136), ([300, 0, 513], 9, 264, 256),
           ([2000], 0, 128, 520), ([7] * 20, 1, 256, 24), ([0, 0, 0], 4, 24, 32), ([90, 700], 0, 520, 776),
-          ([65, 66, 0, 2], 0, 1032, 1536)]
+          ([65, 66, 0, 2], 0, 1032, 1536), ([3, 0, 70, 9] * 50, 2, 136, 264),       # more groups than are ordered
+          ([10, 90, 0, 130] * 10, 0, 520, 520), ([64] * 128, 0, 264, 136)]
 
 
 @pytest.mark.parametrize("sizes,spare,m,n", KGROUP)

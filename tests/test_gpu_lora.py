@@ -19,6 +19,10 @@ CASES = [
     (65, 5, 72, 1032, 24, "runs"), (130, 1, 264, 72, 64, "all"), (300, 3, 136, 520, 128, "runs"),
     (257, 700, 64, 64, 8, "mixed"), (50, 4, 128, 128, 16, "none"), (200, 6, 40, 48, 136, "mixed"),
     (33, 2, 1544, 16, 512, "runs"), (600, 2, 384, 1024, 32, "one"), (0, 3, 64, 64, 16, "all"),
+    # both inner sums in many slices; few tokens an adapter; more columns than a workgroup has at once
+    (700, 2, 4104, 4168, 16, "runs"), (40, 5, 264, 6152, 16, "mixed"), (20, 4, 6152, 520, 200, "mixed"),
+    (30, 3, 1096, 520, 56, "all"), (1600, 100, 2056, 72, 32, "mixed"), (3000, 2, 6152, 40, 80, "mixed"),
+    (1500, 1, 136, 2568, 24, "runs"),
 ]
 
 
@@ -311,3 +315,33 @@ def test_streams_and_graphs():
         for o in outs:
             for x, y in zip(o, want):
                 assert torch.equal(x, y), f"replay {i}"
+
+
+def test_two_calls_at_once():
+    """Two batches on two streams, a workspace each, give what they give alone."""
+    what = "lora two streams"
+    U.banner(what)
+    cases = [Case(what + str(i), m, L, n, k, r, "mixed", BF16) for i, (m, L, n, k, r) in
+             enumerate([(500, 3, 1544, 2056, 16), (90, 40, 2056, 4104, 32)])]
+
+    def run(c, ws, wb):
+        out, v = torch.empty(c.m, c.n, dtype=BF16, device="cuda"), torch.zeros(c.places, c.r, device="cuda")
+        hq.hq_lora(c.x, c.a, c.b, c.sd, c.ends, out, base=c.base, v=v, workspace=ws, **c.kw)
+        dx = torch.empty_like(c.x)
+        da, db = torch.empty(c.L, c.r, c.k, device="cuda"), torch.empty(c.L, c.n, c.r, device="cuda")
+        hq.hq_lora_backward(c.dy, c.x, v, c.a, c.b, c.sd, c.ends, da, db, dx=dx, base=c.dbase, workspace=wb, **c.kw)
+        return out, dx, da, db
+
+    spaces = [(c.ws(), c.ws(True)) for c in cases]
+    alone = [run(c, *s) for c, s in zip(cases, spaces)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        got = []
+        for c, s, stream in zip(cases, spaces, streams):
+            with torch.cuda.stream(stream):
+                got.append(run(c, *s))
+        torch.cuda.synchronize()
+        for want, have in zip(alone, got):
+            for x, y in zip(want, have):
+                assert torch.equal(x, y)
