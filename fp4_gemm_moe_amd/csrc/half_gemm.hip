@@ -79,6 +79,16 @@ int64_t direct_tiles(const HalfGemmArgs& p) {
 
 constexpr int kDirect = -1;      // not a tile: the direct kernel
 
+// Results that the L2s cannot hold leave past them, and the operands stay: 65536
+// rows x 4096 688 -> 685 us, their sums for the weights (805 MB) 737 -> 722 us, 402 MB
+// of such sums 215 -> 219 us, 100 MB as 16 bits (3440 x 1088) 90 -> 82 us.  Only where
+// every row starts a line: lines written in two parts need the L2s (377 MB of 1072 x
+// 2312 FP32 sums 111 -> 152 us past them).
+bool plan_stream(const HalfGemmArgs& p) {
+  const int64_t wide = p.out_kind >= kOutF32 ? 4 : 2, bytes = (p.form == kGroupK ? p.groups : 1) * p.rows * p.n * wide;
+  return bytes > (int64_t)32 << 20 && p.n * wide % 128 == 0 && (uintptr_t)p.out % 128 == 0;
+}
+
 // The kernel and tile of a call, by the rows a group has on average (only the
 // device knows them).  Measured in us, 64 experts of 2048 x 4096 in BF16, T tokens
 // and 8 of the experts each; masked: 32 slots, 4096 x 2048.
@@ -88,18 +98,13 @@ constexpr int kDirect = -1;      // not a tile: the direct kernel
 //    / 103 / 112, of 64 - / 109 / 104; T = 64 - / 177 / 205.  With b [k, n]
 //    (32x64 / 64x128) T = 1 32 / 44, T = 64 186 / 177: the small tile only where
 //    the larger ones are few.
-//  - More: rounds of the chip times what a tile takes.  A 128x128 tile takes 0.32 of a
-//    256x256 one: T = 512 229 (128x128), 284 (256x256), T = 1024 300, 303, T = 2048
-//    424, 398; slots of 128 rows 119, 138; sums over the groups' rows, 8 groups of
-//    128 rows, 1024 x 768: 13.6, 17.4; 64 of 256 rows, 2048 x 1536: 317, 260.
-// Results that the L2s cannot hold leave past them, and the operands stay: 65536
-// rows x 4096 688 -> 685 us, their sums for the weights (805 MB) 737 -> 722 us, 402 MB
-// of such sums 215 -> 219 us.
-bool plan_stream(const HalfGemmArgs& p) {
-  const int64_t bytes = (p.form == kGroupK ? p.groups : 1) * p.rows * p.n * (p.out_kind >= kOutF32 ? 4 : 2);
-  return bytes > (int64_t)32 << 20;
-}
-
+//  - More: rounds of the chip times what a tile takes.  A 128x128 tile takes 0.37 of a
+//    256x256 one (0.28 to 0.47 over many shapes): T = 512 229 (128x128), 284
+//    (256x256), T = 1024 300, 303, T = 2048 424, 398; 8 groups of 1900 rows, 648 x
+//    3128, b [k, n]: 119, 89; slots of 128 rows 119, 138.  Sums over the groups' rows
+//    0.32, since uneven groups leave more of the chip idle in tiles that are few: 10
+//    groups, 18369 rows, 1288 x 584: 52, 88; 8 groups of 128 rows, 1024 x 768: 13.6,
+//    17.4; 31 groups, 21162 rows, 5320 x 1288: 460, 340.
 int plan_half(const HalfGemmArgs& p, const DeviceInfo& dev) {
   const int64_t cus = dev.num_cus;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
@@ -115,7 +120,7 @@ int plan_half(const HalfGemmArgs& p, const DeviceInfo& dev) {
     if (per <= (masked ? 32 : 16) && (!p.b_t || tiles(64, 128) <= 2 * cus)) return kHalf32x64;
     if (per <= (masked ? 64 : 32)) return kHalf64x128;
   }
-  return 0.32 * up(tiles(128, 128), cus) < up(tiles(256, 256), cus) ? kHalf128x128 : kHalf256x256;
+  return (p.form == kGroupK ? 0.32 : 0.37) * up(tiles(128, 128), cus) < up(tiles(256, 256), cus) ? kHalf128x128 : kHalf256x256;
 }
 
 }  // namespace
