@@ -761,9 +761,11 @@ struct OuterArgs {
   const float* u;          // [slices, max_rows, r]
   const uint16_t* z;       // [m, k]
   float* part;             // [chunks, r, k]; UT: [chunks, k, r]
+  float* out;              // [adapters, r, k]; UT: [adapters, k, r]
   int k, r, slices;
   int places;              // of a chunk
   unsigned tiles;          // workgroups
+  bool accumulate;
 };
 constexpr int kOuterCols = 256, kOuterRows = 32;
 
@@ -901,15 +903,23 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
       }
     }
   }
+  // an adapter's only chunk is its result; else lora_sum joins them
+  const bool whole = t.index == t.first && t.row_end - t.row0 <= p.places, add = whole && p.accumulate;
+  const float f = whole && p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
+  float* out = (whole ? p.out + (int64_t)t.g * p.r * p.k : p.part + (int64_t)t.index * p.r * p.k);
   // four neighbours of a lane: columns (rank x) or, UT, ranks (column x)
-  float* out = p.part + (int64_t)t.index * p.r * p.k;
 #pragma unroll
   for (int i = 0; i < RF; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int rank = i0 + 16 * i + (UT ? 4 * q : x), col = j0 + 64 * w + 16 * j + (UT ? x : 4 * q);
-      if (rank < p.r && col < p.k)
-        *reinterpret_cast<v4f*>(out + (UT ? (int64_t)col * p.r + rank : (int64_t)rank * p.k + col)) = acc[i][j];
+      if (rank >= p.r || col >= p.k) continue;
+      v4f* d = reinterpret_cast<v4f*>(out + (UT ? (int64_t)col * p.r + rank : (int64_t)rank * p.k + col));
+      v4f v = acc[i][j];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= f;
+      if (add) v += *d;
+      *d = v;
     }
 }
 
@@ -936,7 +946,8 @@ __global__ __launch_bounds__(kThreads, 2) void lora_back(BackArgs p) {
   else expand_few<F16, true, RF>(p.dx, (int)id);
 }
 
-// da, db: scale times the sum of an adapter's chunks, in order.
+// da, db: scale times the sum of an adapter's chunks, in order, where it has several;
+// zeros where it has none.
 struct SumArgs {
   LoraPlan pl;
   const float *pa, *pb;
@@ -955,7 +966,7 @@ __global__ __launch_bounds__(kThreads) void lora_sum(SumArgs p) {
   const int64_t n = b ? p.nb : p.na, i = b ? at - p.na : at;
   const int chunks = (t.row_end - t.row0 + p.places - 1) / p.places;
   v4f* out = reinterpret_cast<v4f*>((b ? p.db : p.da) + g * n + i);
-  if (p.accumulate && chunks == 0) return;
+  if (chunks == 1 || (p.accumulate && chunks == 0)) return;
   const float* src = (b ? p.pb : p.pa) + t.first * n + i;
   v4f s = {0, 0, 0, 0};
   for (int c = 0; c < chunks; ++c) s += *reinterpret_cast<const v4f*>(src + c * n);
@@ -992,10 +1003,11 @@ ShrinkPlan shrink_plan(int64_t max_rows, int64_t adapters, int64_t k, int64_t r)
 }
 // Places of a workgroup: 16 where an adapter has few on average, else 64.
 int expand_places(int64_t max_rows, int64_t adapters) { return max_rows <= 16 * adapters ? 16 : 64; }
+// Steps of 16 ranks whose fragments a wave keeps.
 int expand_steps(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 // Columns of a workgroup: what makes about 2 kFill workgroups, whole 256s.
 int expand_chunk(int64_t tiles, int64_t n) {
-  const int64_t across = tiles > 0 ? up(2 * kFill, tiles) : 1;
+    const int64_t across = tiles > 0 ? up(2 * kFill, tiles) : 1;
   return (int)(up(up(n, across), 256) * 256);
 }
 int outer_rf(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
@@ -1075,21 +1087,22 @@ hipError_t expand_one(hipStream_t s, const ExpandArgs& p) {
   hipLaunchKernelGGL((lora_expand<F16, WT, STEPS, MANY>), dim3(p.tiles + p.rest), dim3(kThreads), bytes, s, p);
   return hipGetLastError();
 }
-template <bool F16, bool WT, int STEPS>
-hipError_t expand_steps(hipStream_t s, const ExpandArgs& p) {
-  return expand_places(p.pl.max_rows, p.pl.adapters) == 16 ? expand_one<F16, WT, STEPS, false>(s, p)
-                                                          : expand_one<F16, WT, STEPS, true>(s, p);
-}
 template <bool F16, bool WT>
 hipError_t expand(hipStream_t s, const ExpandArgs& p) {
-  const int steps = expand_steps(p.r);
-  return steps == 1 ? expand_steps<F16, WT, 1>(s, p) : steps == 2 ? expand_steps<F16, WT, 2>(s, p) : expand_steps<F16, WT, 4>(s, p);
+  const bool many = expand_places(p.pl.max_rows, p.pl.adapters) == 64;
+  switch (expand_steps(p.r)) {
+    case 1: return many ? expand_one<F16, WT, 1, true>(s, p) : expand_one<F16, WT, 1, false>(s, p);
+    case 2: return many ? expand_one<F16, WT, 2, true>(s, p) : expand_one<F16, WT, 2, false>(s, p);
+    default: return many ? expand_one<F16, WT, 4, true>(s, p) : expand_one<F16, WT, 4, false>(s, p);
+  }
 }
-// One launch does it: few places an adapter, ranks that a wave's registers hold,
-// no more workgroups than the chip takes at once, and an A that one compute unit
-// reads in about a launch's time (every workgroup reads all of its adapter's).
+// One launch does it: few places an adapter, ranks that a wave's registers hold (of
+// 64 one launch takes 14.1 us where two take 12.7, of 32 10.4 and 13.2), no more
+// workgroups than the chip takes at once, and an A that one compute unit reads in about
+// a launch's time (every workgroup reads all of its adapter's; 16 ranks of 6000
+// values 12.5 us, 13.3).
 bool one_launch(const LoraPlan& pl, int64_t n, int64_t k, int64_t r) {
-  return pl.max_rows <= 16 * pl.adapters && r <= 64 && r * k <= 3 << 15 &&
+  return pl.max_rows <= 16 * pl.adapters && r <= 32 && r * k <= 3 << 15 &&
          tile_bound(pl.max_rows, pl.adapters, 16) * up(n, kOneWaves * 64) <= kFill / 2;
 }
 template <bool F16, int STEPS>
@@ -1111,8 +1124,7 @@ hipError_t forward(hipStream_t s, const LoraArgs& p) {
     x.chunk = kOneWaves * 64;
     x.chunks = (int)up(p.n, x.chunk);
     x.tiles = (unsigned)(tile_bound(pl.max_rows, pl.adapters, 16) * x.chunks);
-    const int steps = expand_steps(p.r);
-    return steps == 1 ? one<F16, 1>(s, a, x) : steps == 2 ? one<F16, 2>(s, a, x) : one<F16, 4>(s, a, x);
+    return p.r <= 16 ? one<F16, 1>(s, a, x) : one<F16, 2>(s, a, x);
   }
   const ShrinkPlan plan = shrink_plan(pl.max_rows, pl.adapters, p.k, p.r);
   // the workspace: the slices (if any), then v where it is not kept
@@ -1152,8 +1164,9 @@ hipError_t back_one(hipStream_t s, const BackArgs& p) {
 }
 template <bool F16, int RF>
 hipError_t back(hipStream_t s, const BackArgs& p, const LoraPlan& pl) {
+  const bool many = expand_places(pl.max_rows, pl.adapters) == 64;
   if (p.dx.out != nullptr && (int64_t)p.da.tiles + p.db.tiles + p.dx.tiles <= 2 * kFill)
-    return expand_places(pl.max_rows, pl.adapters) == 16 ? back_one<F16, RF, false>(s, p) : back_one<F16, RF, true>(s, p);
+    return many ? back_one<F16, RF, true>(s, p) : back_one<F16, RF, false>(s, p);
   const hipError_t e = outer<F16, RF>(s, p);
   return e != hipSuccess || p.dx.out == nullptr ? e : expand<F16, true>(s, p.dx);
 }
@@ -1173,8 +1186,10 @@ hipError_t backward(hipStream_t s, const LoraArgs& p) {
   const int places = outer_places(pl.max_rows, p.n, p.k, p.r);
   const int64_t each = tile_bound(pl.max_rows, pl.adapters, places) * up(p.r, 16 * outer_rf(p.r));
   BackArgs x;
-  x.da = OuterArgs{pl, u, p.x, pa, (int)p.k, (int)p.r, slices, places, (unsigned)(each * up(p.k, kOuterCols))};
-  x.db = OuterArgs{pl, p.v, p.dy, pb, (int)p.n, (int)p.r, 1, places, (unsigned)(each * up(p.n, kOuterCols))};
+  x.da = OuterArgs{pl, u, p.x, pa, p.da, (int)p.k, (int)p.r, slices, places, (unsigned)(each * up(p.k, kOuterCols)),
+                   p.accumulate};
+  x.db = OuterArgs{pl, p.v, p.dy, pb, p.db, (int)p.n, (int)p.r, 1, places, (unsigned)(each * up(p.n, kOuterCols)),
+                   p.accumulate};
   x.dx = expand_args(pl, u, p.a, p.base, p.out, nullptr, p.k, p.r, slices);
   const int rf = outer_rf(p.r);
   e = rf == 1 ? back<F16, 1>(s, x, pl) : rf == 2 ? back<F16, 2>(s, x, pl) : back<F16, 4>(s, x, pl);
