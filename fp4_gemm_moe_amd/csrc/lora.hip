@@ -423,9 +423,9 @@ struct Places {
   }
 };
 
-// Eight results of a lane: columns n .. + 7 of its place's token.
+// Eight results of a lane.
 template <bool F16>
-__device__ __forceinline__ void expand_store(uint16_t* d, v4i base, v4f a, v4f b, float back) {
+__device__ __forceinline__ v4i expand_result(v4i base, v4f a, v4f b, float back) {
   const float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   v4i o;
 #pragma unroll
@@ -434,7 +434,19 @@ __device__ __forceinline__ void expand_store(uint16_t* d, v4i base, v4f a, v4f b
     o[e] = (int)pack_half2<F16>(__builtin_fmaf(f[2 * e], back, half_lo<F16>(u)),
                                 __builtin_fmaf(f[2 * e + 1], back, half_hi<F16>(u)));
   }
-  *reinterpret_cast<v4i*>(d) = o;
+  return o;
+}
+
+// Lanes of two neighbouring places trade a for b, so that what each had for 64
+// neighbouring columns of its own row becomes 32 columns of the even place's row and
+// 32 of the odd one's, and eight lanes a whole line of 128 bytes; and back again.
+__device__ __forceinline__ void trade(bool odd, v4i& a, v4i& b) {
+  const v4i mine = odd ? a : b;
+  v4i other;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) other[e] = __builtin_amdgcn_mov_dpp(mine[e], 0xB1, 0xf, 0xf, false);   // quad_perm:[1,0,3,2]
+  if (odd) a = other;
+  else b = other;
 }
 
 // The columns of fragment j of a lane's pairs: 32 (j / 2) + 8 (x / 4) + 4 (j % 2) + x %
@@ -473,12 +485,16 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& p, int id) {
         }
       }
   };
+  // base and results by whole lines, as expand_many has them
+  const bool odd = x & 1;
+  const int64_t other = __shfl_xor((long long)pl.tok, 1, 64);
+  const int64_t tok[2] = {odd ? other : pl.tok, odd ? pl.tok : other};
   auto fetch_base = [&](int n0) {
+    const int col = n0 + 32 * odd + 8 * q;
 #pragma unroll
-    for (int jp = 0; jp < 2; ++jp) {
-      const int col = n0 + 32 * jp + 8 * q;
-      base[jp] = v4i{0, 0, 0, 0};
-      if (p.base != nullptr && pl.tok >= 0 && col < c1) base[jp] = load8(p.base + pl.tok * p.n + col);
+    for (int h = 0; h < 2; ++h) {
+      base[h] = v4i{0, 0, 0, 0};
+      if (p.base != nullptr && tok[h] >= 0 && col < c1) base[h] = load8(p.base + tok[h] * p.n + col);
     }
   };
   pl.start(p, scale, p.v_out != nullptr && c0 == 0 && w == 0);
@@ -516,12 +532,13 @@ __device__ __forceinline__ void expand_few(const ExpandArgs& p, int id) {
       if (16 * (s0 + STEPS) < p.r) fetch(n0, s0 + STEPS);
       else if (n0 + 256 < c1) fetch(n0 + 256, 0);
     }
+    trade(odd, base[0], base[1]);
+    v4i o[2] = {expand_result<F16>(base[0], acc[0], acc[1], pl.back), expand_result<F16>(base[1], acc[2], acc[3], pl.back)};
+    trade(odd, o[0], o[1]);
+    const int col = n0 + 32 * odd + 8 * q;
 #pragma unroll
-    for (int jp = 0; jp < 2; ++jp) {
-      const int col = n0 + 32 * jp + 8 * q;
-      if (pl.tok >= 0 && col < c1)
-        expand_store<F16>(p.out + pl.tok * p.n + col, base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
-    }
+    for (int h = 0; h < 2; ++h)
+      if (tok[h] >= 0 && col < c1) *reinterpret_cast<v4i*>(p.out + tok[h] * p.n + col) = o[h];
     if (n0 + 256 < c1) fetch_base(n0 + 256);
   }
 }
@@ -566,14 +583,19 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& p, int id) {
   Places<F16, STEPS, STEPS == 4 ? 1 : 2> pl;
   pl.find(p, t, t.row0 + 16 * w);
   pl.start(p, scale, p.v_out != nullptr && c0 == 0);
+  // the even and the odd place's tokens, and the lane's columns of both (jp even: one pair of 64)
+  const bool odd = x & 1;
+  const int64_t other = __shfl_xor((long long)pl.tok, 1, 64);
+  const int64_t first = odd ? other : pl.tok, second = odd ? pl.tok : other;
+  auto column = [&](int n0, int jp) { return n0 + 32 * ((jp & ~1) + odd) + 8 * q; };
   int buf = 0;
   for (int n0 = c0; n0 < c1; n0 += 256) {
-    v4i base[8];
+    v4i base[8];                         // traded
 #pragma unroll
     for (int jp = 0; jp < 8; ++jp) {
-      const int col = n0 + 32 * jp + 8 * q;
+      const int64_t tok = jp & 1 ? second : first;
       base[jp] = v4i{0, 0, 0, 0};
-      if (p.base != nullptr && pl.tok >= 0 && col < c1) base[jp] = load8(p.base + pl.tok * p.n + col);
+      if (p.base != nullptr && tok >= 0 && column(n0, jp) < c1) base[jp] = load8(p.base + tok * p.n + column(n0, jp));
     }
     v4f acc[16];
 #pragma unroll
@@ -613,10 +635,14 @@ __device__ __forceinline__ void expand_many(const ExpandArgs& p, int id) {
       }
     }
 #pragma unroll
-    for (int jp = 0; jp < 8; ++jp) {
-      const int col = n0 + 32 * jp + 8 * q;
-      if (pl.tok >= 0 && col < c1)
-        expand_store<F16>(p.out + pl.tok * p.n + col, base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
+    for (int jp = 0; jp < 8; jp += 2) {
+      trade(odd, base[jp], base[jp + 1]);
+      v4i a = expand_result<F16>(base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
+      v4i b = expand_result<F16>(base[jp + 1], acc[2 * jp + 2], acc[2 * jp + 3], pl.back);
+      trade(odd, a, b);
+      const int col = column(n0, jp);
+      if (first >= 0 && col < c1) *reinterpret_cast<v4i*>(p.out + first * p.n + col) = a;
+      if (second >= 0 && col < c1) *reinterpret_cast<v4i*>(p.out + second * p.n + col) = b;
     }
   }
 }
@@ -745,7 +771,8 @@ __global__ __launch_bounds__(kOneWaves * 64) void lora_one(ShrinkArgs a, ExpandA
   for (int jp = 0; jp < 2; ++jp) {
     const int col = n0 + 32 * jp + 8 * q;
     if (pl.tok >= 0 && col < p.n)
-      expand_store<F16>(p.out + pl.tok * p.n + col, base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
+      *reinterpret_cast<v4i*>(p.out + pl.tok * p.n + col) =
+          expand_result<F16>(base[jp], acc[2 * jp], acc[2 * jp + 1], pl.back);
   }
 }
 
@@ -1007,7 +1034,7 @@ int expand_places(int64_t max_rows, int64_t adapters) { return max_rows <= 16 * 
 int expand_steps(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 // Columns of a workgroup: what makes about 2 kFill workgroups, whole 256s.
 int expand_chunk(int64_t tiles, int64_t n) {
-    const int64_t across = tiles > 0 ? up(2 * kFill, tiles) : 1;
+  const int64_t across = tiles > 0 ? up(2 * kFill, tiles) : 1;
   return (int)(up(up(n, across), 256) * 256);
 }
 int outer_rf(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
