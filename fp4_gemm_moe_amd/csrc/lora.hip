@@ -283,19 +283,31 @@ __device__ __forceinline__ void expand_rest(const ExpandArgs& p, int id) {
     const int64_t place = p.pl.row_map != nullptr ? p.pl.row_map[t0 + lane] : t0 + lane;
     none = place < 0 || place >= last;
   }
-  uint64_t left = __ballot(none);
-  for (int i = 0; left != 0; ++i, left &= left - 1) {
-    if ((i & 3) != wave) continue;
-    const int64_t at = (t0 + __builtin_ctzll(left)) * p.n;
-    v4i v[kRestCols / 512];
+  // every fourth of them is this wave's; four at a time, or the loads' latency of each adds up
+  uint64_t all = __ballot(none), mine = 0;
+  for (int i = 0; all != 0; ++i, all &= all - 1)
+    if ((i & 3) == wave) mine |= all & -all;
+  constexpr int ROWS = 4, PIECES = kRestCols / 512;
+  while (mine != 0) {
+    int64_t at[ROWS];                    // -1: no row
 #pragma unroll
-    for (int e = 0; e < kRestCols / 512; ++e) {
-      v[e] = v4i{0, 0, 0, 0};
-      if (p.base != nullptr && c0 + lane * 8 + 512 * e < p.n) v[e] = load8(p.base + at + c0 + lane * 8 + 512 * e);
-    }
+    for (int i = 0; i < ROWS; ++i, mine &= mine - 1) at[i] = mine != 0 ? (t0 + __builtin_ctzll(mine)) * p.n : -1;
+    v4i v[ROWS][PIECES];
 #pragma unroll
-    for (int e = 0; e < kRestCols / 512; ++e)
-      if (c0 + lane * 8 + 512 * e < p.n) *reinterpret_cast<v4i*>(p.out + at + c0 + lane * 8 + 512 * e) = v[e];
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+      for (int e = 0; e < PIECES; ++e) {
+        const int col = c0 + lane * 8 + 512 * e;
+        v[i][e] = v4i{0, 0, 0, 0};
+        if (p.base != nullptr && at[i] >= 0 && col < p.n) v[i][e] = load8(p.base + at[i] + col);
+      }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+      for (int e = 0; e < PIECES; ++e) {
+        const int col = c0 + lane * 8 + 512 * e;
+        if (at[i] >= 0 && col < p.n) *reinterpret_cast<v4i*>(p.out + at[i] + col) = v[i][e];
+      }
   }
 }
 
@@ -951,7 +963,9 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
 }
 
 // dA's and dB's chunks in one launch; where they are few, dx's tiles too (its
-// registers would keep the chunks from filling the chip).
+// registers would keep the chunks from filling the chip; three workgroups a compute
+// unit where 16 ranks allow it: 2918 tokens, 1568 + 1344 wide, 33.0 -> 28.6 us, while
+// dx alone is better off with two, 4096 places of 17408 columns 76 us against 81).
 struct BackArgs {
   OuterArgs da, db;
   ExpandArgs dx;
@@ -962,7 +976,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer(BackArgs p) {
   else outer_tile<F16, true, RF>(p.db, (int)(blockIdx.x - p.da.tiles));
 }
 template <bool F16, int RF, bool MANY>
-__global__ __launch_bounds__(kThreads, 2) void lora_back(BackArgs p) {
+__global__ __launch_bounds__(kThreads, RF == 1 ? 3 : 2) void lora_back(BackArgs p) {
   unsigned id = blockIdx.x;
   if (id < p.da.tiles) return outer_tile<F16, false, RF>(p.da, (int)id);
   id -= p.da.tiles;
