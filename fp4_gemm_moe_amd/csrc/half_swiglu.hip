@@ -7,7 +7,8 @@
 //
 // Memory bounds both: 6 bytes move for each y, 10 for each y of the gradient, 12
 // where it writes y too.  A thread takes eight neighbouring values of a row, in
-// 16-byte words.
+// 16-byte words: 65536 x 1536 with y 213 us, 5.67 TB/s (a copy of 256 MB 5.4); 512 x
+// 2048 3.2 us, one launch's latency.
 #include "block_fmt.hpp"
 #include "half_internal.hpp"
 #include "sched.hpp"

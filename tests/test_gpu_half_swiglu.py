@@ -152,3 +152,22 @@ def test_gradient_against_differences():
         up = np.abs(xv[:, 64:]) if half == 0 else 1.0
         bound = step ** 2 * np.abs(dyv) * up + (2.0 ** -11 + 2.0 ** -16) * np.abs(diff) + 2.0 ** -16 * np.abs(dyv) * up + 2.0 ** -24
         H.check(got, diff, bound, f"half {half}")
+
+
+def test_binding_refuses():
+    """Wrong types, sizes and selections of device tensors, before a launch."""
+    x, y = torch.zeros(6, 32, dtype=BF16, device="cuda"), torch.full((6, 16), F.MARK, dtype=BF16, device="cuda")
+    ends = torch.tensor([2, 6], dtype=torch.int32, device="cuda")
+    for bad in (dict(group_end=ends[:0]), dict(valid=ends), dict(group_end=ends, num_groups=3), dict(group_end=ends.long()),
+                dict(group_end=ends, valid=ends[:1]), dict(group_end=ends.cpu())):
+        with pytest.raises(ValueError):
+            hq.hq_swiglu(x, y, **bad)
+    for bad in ((x, y.half()), (x, y[:5]), (x.float(), y), (x.t(), y), (x, y.t())):
+        with pytest.raises(ValueError):
+            hq.hq_swiglu(*bad)
+    with pytest.raises(ValueError):
+        hq.hq_swiglu_backward(y, x, x[:, :16])
+    with pytest.raises(hq.HQError):
+        hq.hq_swiglu(x, y, num_groups=2)              # neither ends nor slots
+    torch.cuda.synchronize()
+    assert torch.all(y == F.MARK)
