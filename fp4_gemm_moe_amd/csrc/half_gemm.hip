@@ -105,6 +105,11 @@ bool plan_stream(const HalfGemmArgs& p) {
 //    0.32, since uneven groups leave more of the chip idle in tiles that are few: 10
 //    groups, 18369 rows, 1288 x 584: 52, 88; 8 groups of 128 rows, 1024 x 768: 13.6,
 //    17.4; 31 groups, 21162 rows, 5320 x 1288: 460, 340.
+//  - Between them 128x256 tiles, for rows only, at 0.65 of a large one: 954 rows of 9
+//    groups, 4192 x 816: 27.6 (256x256), 19.5, 23.0 (128x128); 1589 of 14, 5856 x 5328,
+//    b [k, n]: 222, 280 (128x128).  Not where groups have up to 64 rows, each weight is
+//    read once and two stages keep too few loads under way: T = 512 255, 229
+//    (128x128); nor for sums (8056 rows of 12 groups, 2344 x 4432: 288, 236 (256x256)).
 int plan_half(const HalfGemmArgs& p, const DeviceInfo& dev) {
   const int64_t cus = dev.num_cus;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
@@ -120,7 +125,12 @@ int plan_half(const HalfGemmArgs& p, const DeviceInfo& dev) {
     if (per <= (masked ? 32 : 16) && (!p.b_t || tiles(64, 128) <= 2 * cus)) return kHalf32x64;
     if (per <= (masked ? 64 : 32)) return kHalf64x128;
   }
-  return (p.form == kGroupK ? 0.32 : 0.37) * up(tiles(128, 128), cus) < up(tiles(256, 256), cus) ? kHalf128x128 : kHalf256x256;
+  const double large = (double)up(tiles(256, 256), cus), small = (p.form == kGroupK ? 0.32 : 0.37) * up(tiles(128, 128), cus);
+  if (p.form != kGroupK && (p.form == kMasked ? p.slot_rows / 2 : p.rows / p.groups) > 64) {
+    const double half = 0.65 * up(tiles(128, 256), cus);
+    if (half < large && half < small) return kHalf128x256;
+  }
+  return small < large ? kHalf128x128 : kHalf256x256;
 }
 
 }  // namespace

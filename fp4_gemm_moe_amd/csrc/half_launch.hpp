@@ -8,7 +8,7 @@
 namespace hq {
 
 // Tile shapes of the tiled kernel (rows x columns).
-enum HalfTile : int { kHalf256x256, kHalf128x128, kHalf64x128, kHalf32x64 };
+enum HalfTile : int { kHalf256x256, kHalf128x256, kHalf128x128, kHalf64x128, kHalf32x64 };
 
 // One launch with the operands as the products have them: a and b K-minor (nt),
 // b K-major outside (nn), both (tn, the form that sums over the groups' rows).
@@ -54,6 +54,9 @@ template <bool AT, bool BT>
 hipError_t launch_tile(hipStream_t s, const HalfGemmArgs& p, const DeviceInfo& dev, int tile) {
   switch (tile) {
     case kHalf256x256: return launch_type<Cfg<256, 256, 2, 2, 2>, AT, BT>(s, p, dev);
+    case kHalf128x256:
+      if constexpr (!AT) return launch_type<Cfg<128, 256, 2, 2, 2>, AT, BT>(s, p, dev);
+      return hipErrorInvalidValue;       // not planned for sums over the rows
     case kHalf128x128: return launch_type<Cfg<128, 128, 2, 2, 4>, AT, BT>(s, p, dev);
     case kHalf64x128: return launch_type<Cfg<64, 128, 1, 4, 5>, AT, BT>(s, p, dev);
     default: return launch_type<Cfg<32, 64, 1, 2, 9>, AT, BT>(s, p, dev);
