@@ -246,14 +246,19 @@ __global__ __launch_bounds__(256) void lora_shrink_many(ShrinkArgs p) {
   }
 }
 
-// The sum of the slices' partial sums, in order, for every place with a token.
+// The sum of the slices' partial sums, in order, for every place with a token: those
+// from the last end on have none, whatever token_at says (without a map it knows only
+// m), and no partial sums.  The sums are read before the token and the ends have
+// come (they lie in the workspace either way) and only the store waits for them.
 __global__ __launch_bounds__(256) void lora_slices(LoraPlan pl, const float* part, int r, int slices, float* out) {
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = pl.max_rows * r;
-  if (at >= all || token_at(pl, (int)(at / r)) < 0) return;
+  const int place = (int)(at / r);
   v4f v[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e)
-    if (e < slices) v[e] = *reinterpret_cast<const v4f*>(part + e * all + at);
+    if (e < slices && at < all) v[e] = *reinterpret_cast<const v4f*>(part + e * all + at);
+  const int last = last_end(pl.group_end, pl.adapters, (int)pl.max_rows);       // by whole waves
+  if (at >= all || place >= last || token_at(pl, place) < 0) return;
   v4f s = v[0];
 #pragma unroll
   for (int e = 1; e < 16; ++e)
