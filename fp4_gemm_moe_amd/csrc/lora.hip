@@ -820,6 +820,17 @@ struct OuterArgs {
 };
 constexpr int kOuterCols = 256, kOuterRows = 32;
 
+// The scale of adapter g's sums.  One that is not finite counts only where one of its
+// places holds a token: the gradients of an adapter without tokens are zeros, and 0
+// times an infinity or NaN is not.  Uniform arguments, all lanes of the wave.
+__device__ __forceinline__ float sum_scale(const LoraPlan& pl, int g, int row0, int row_end) {
+  const float f = pl.scale != nullptr ? pl.scale[g] : 1.0f;
+  if (__builtin_fabsf(f) < INFINITY) return f;
+  bool any = false;
+  for (int place = row0 + (int)(threadIdx.x & 63); place < row_end && !any; place += 64) any = token_at(pl, place) >= 0;
+  return __ballot(any) != 0 ? f : 0.0f;
+}
+
 template <int RF>
 constexpr int outer_smem() { return kOuterRows * (kOuterCols * 2 + 16) + 3 * kOuterRows * (RF * 32 + 16); }
 
@@ -956,7 +967,7 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
   }
   // an adapter's only chunk is its result; else lora_sum joins them
   const bool whole = t.index == t.first && t.row_end - t.row0 <= p.places, add = whole && p.accumulate;
-  const float f = whole && p.pl.scale != nullptr ? p.pl.scale[t.g] : 1.0f;
+  const float f = whole ? sum_scale(p.pl, t.g, t.row0, t.row_end) : 1.0f;
   float* out = (whole ? p.out + (int64_t)t.g * p.r * p.k : p.part + (int64_t)t.index * p.r * p.k);
   // four neighbours of a lane: columns (rank x) or, UT, ranks (column x)
 #pragma unroll
@@ -1014,6 +1025,7 @@ __global__ __launch_bounds__(kThreads) void lora_sum(SumArgs p) {
   const int g = (int)(blockIdx.x / p.blocks);
   const int64_t at = ((int64_t)(blockIdx.x % p.blocks) * kThreads + threadIdx.x) * 4;
   const GroupTile t = group_tile<true>(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, p.places, g);
+  const float f = sum_scale(p.pl, g, t.row0, t.row_end);
   if (at >= p.na + p.nb) return;
   const bool b = at >= p.na;
   const int64_t n = b ? p.nb : p.na, i = b ? at - p.na : at;
@@ -1023,7 +1035,6 @@ __global__ __launch_bounds__(kThreads) void lora_sum(SumArgs p) {
   const float* src = (b ? p.pb : p.pa) + t.first * n + i;
   v4f s = {0, 0, 0, 0};
   for (int c = 0; c < chunks; ++c) s += *reinterpret_cast<const v4f*>(src + c * n);
-  const float f = p.pl.scale != nullptr ? p.pl.scale[g] : 1.0f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) s[e] *= f;
   if (p.accumulate) s += *out;

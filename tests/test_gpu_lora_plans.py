@@ -52,3 +52,38 @@ def test_rows_past_the_last_end(m, L, n, k, r, dtype):
     bound = ((k + r + 32) * 2.0 ** -23 + 2.0 ** -16) * ref["mag"] + H.UNIT[dtype] * np.abs(ref["out"]) + H.FLOOR[dtype]
     H.check(out, ref["out"], bound, what)
     assert torch.equal(out[last:], base[last:])
+
+
+@pytest.mark.parametrize("unused", [float("nan"), float("inf"), -2.0])
+@pytest.mark.parametrize("m,align", [(40, 1), (40, 16), (3000, 1), (3000, 16)])
+def test_an_unused_adapters_scale(unused, m, align):
+    """da and db of an adapter without tokens are zeros whatever its scale, also
+    where its places are there but hold no token; the others are as they were."""
+    what = f"lora unused scale {unused} m={m} align={align}"
+    U.banner(what)
+    L, n, k, r = 5, 136, 264, 16
+    g = H.rng(what)
+    ids = g.choice([0, 2, 3], m).astype(np.int64)
+    row_map, row_pair, ends, _ = hq.moe_sort(H.dev(ids).view(-1, 1), L, align)
+    if align > 1:           # adapter 4 gets all the places that are left, without a token
+        ends[4] = row_pair.numel()
+    x, dy = F.halves(g, (m, k), BF16)[0], F.halves(g, (m, n), BF16)[0]
+    a, b = F.halves(g, (L, r, k), BF16)[0], F.halves(g, (L, n, r), BF16)[0]
+    v = torch.randn(row_pair.numel(), r, device="cuda")
+    space = _workspace(hq.hq_lora_backward_workspace_size(m, n, k, r, L, row_pair.numel()))
+    got = []
+    for s in (1.5, unused):
+        scale = torch.tensor([1.5, s, 1.5, 1.5, s], device="cuda")
+        da, db = torch.empty(L, r, k, device="cuda"), torch.empty(L, n, r, device="cuda")
+        hq.hq_lora_backward(dy, x, v, a, b, scale, ends, da, db, row_map=row_map, row_pair=row_pair, workspace=space)
+        got.append((da, db))
+    for before, after in zip(*got):
+        assert torch.all(after[[1, 4]] == 0), f"{what}: gradients of an adapter without tokens"
+        assert torch.equal(before[[0, 2, 3]], after[[0, 2, 3]])
+    # one that has tokens does get its scale
+    scale = torch.full((L,), unused, device="cuda")
+    hq.hq_lora_backward(dy, x, v, a, b, scale, ends, da, db, row_map=row_map, row_pair=row_pair, workspace=space)
+    if np.isfinite(unused):
+        assert torch.equal(da, got[0][0] * (unused / 1.5)) or torch.allclose(da, got[0][0] * (unused / 1.5), rtol=1e-6)
+    else:
+        assert not torch.isfinite(da[[0, 2, 3]]).any() and not torch.isfinite(db[[0, 2, 3]]).any()
