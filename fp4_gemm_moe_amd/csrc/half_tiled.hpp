@@ -471,12 +471,16 @@ __global__ __launch_bounds__(C::THREADS, 1) void half_gemm_tiled(HalfGemmArgs p)
     };
     constexpr std::true_type yes;
     constexpr std::false_type no;
-    if (p.out_kind == kOutF32Add) store(std::integral_constant<int, 4>(), yes, no);
+    stored = true;
+    if (p.out_kind == kOutF32Add) {
+      // a group without rows adds nothing: its result is not even read (another stream may be adding to it)
+      if (AT && ufirst((uint32_t)table.end[t.g]) == ufirst((uint32_t)(t.g > 0 ? table.end[t.g - 1] : 0))) stored = false;
+      else store(std::integral_constant<int, 4>(), yes, no);
+    }
     else if (p.out_kind == kOutF32 && p.stream) store(std::integral_constant<int, 4>(), no, yes);
     else if (p.out_kind == kOutF32) store(std::integral_constant<int, 4>(), no, no);
     else if (p.stream) store(std::integral_constant<int, 2>(), no, yes);
     else store(std::integral_constant<int, 2>(), no, no);
-    stored = true;
   }
   wait_vm<0>();       // no load may land in LDS after the workgroup has ended
 }
