@@ -107,7 +107,8 @@ hq_status check_lora(const char* what, const hq::LoraArgs& p, uint64_t need, uin
     return fail(HQ_ERR_SHAPE, "%s: problem too large (a launch would pass 2^32 work items)", what);
   if ((pl.row_map != nullptr) != (pl.row_pair != nullptr) && pl.m > 0 && pl.max_rows > 0)
     return fail(HQ_ERR_NULL, "%s: row_map and row_pair go together", what);
-  if (pl.row_pair == nullptr && pl.max_rows != pl.m)
+  const bool no_places = pl.row_map != nullptr && pl.max_rows == 0;      // row_pair is empty, and may be NULL
+  if (pl.row_pair == nullptr && pl.max_rows != pl.m && !no_places)
     return fail(HQ_ERR_SHAPE, "%s: without row_pair max_rows=%lld must be m=%lld", what, (long long)pl.max_rows,
                 (long long)pl.m);
   if (!pl.group_end) return fail(HQ_ERR_NULL, "%s: group_end is required", what);

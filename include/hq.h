@@ -728,7 +728,8 @@ hq_status hq_swiglu_backward(void* stream, const uint16_t* dy, const uint16_t* x
  * group_end[g] have g, those past the last end none.  Ends are clamped to
  * non-decreasing ones in [0, max_rows], entries of row_pair outside [0, m) hold
  * no token and those of row_map outside [0, the last end) no place; no token may
- * have two places.
+ * have two places.  With a row_map and max_rows == 0 no token has an adapter, and
+ * row_pair and v, which are empty, may be NULL.
  *   v  [max_rows, r] FP32 (NULL: not kept): x A^T by place, which the gradients
  *      need; places without a token are not written.
  * r % 8 == 0, 8 <= r <= 512; n % 8 == 0, k % 8 == 0, both below 2^21 and

@@ -87,3 +87,28 @@ def test_an_unused_adapters_scale(unused, m, align):
         assert torch.equal(da, got[0][0] * (unused / 1.5)) or torch.allclose(da, got[0][0] * (unused / 1.5), rtol=1e-6)
     else:
         assert not torch.isfinite(da[[0, 2, 3]]).any() and not torch.isfinite(db[[0, 2, 3]]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_no_places(dtype):
+    """A map that holds no place: every token is without an adapter."""
+    U.banner(f"lora no places {dtype}")
+    m, L, n, k, r = 70, 3, 136, 72, 16
+    g = H.rng("no places", str(dtype))
+    x, base = F.halves(g, (m, k), dtype)[0], F.halves(g, (m, n), dtype)[0]
+    a, b = F.halves(g, (L, r, k), dtype)[0], F.halves(g, (L, n, r), dtype)[0]
+    ends = torch.zeros(L, dtype=torch.int32, device="cuda")
+    kw = dict(row_map=torch.full((m,), -1, dtype=torch.int32, device="cuda"),
+              row_pair=torch.empty(0, dtype=torch.int32, device="cuda"))
+    v = torch.empty(0, r, device="cuda")
+    out = torch.full((m, n), F.MARK, dtype=dtype, device="cuda")
+    hq.hq_lora(x, a, b, None, ends, out, base=base, v=v, **kw)
+    assert torch.equal(out, base)
+    hq.hq_lora(x, a, b, None, ends, out, **kw)
+    assert torch.all(out == 0)
+    dx = torch.full((m, k), F.MARK, dtype=dtype, device="cuda")
+    da, db = torch.full((L, r, k), F.MARK, device="cuda"), torch.full((L, n, r), F.MARK, device="cuda")
+    hq.hq_lora_backward(base, x, v, a, b, None, ends, da, db, dx=dx, base=x, **kw)
+    assert torch.equal(dx, x) and torch.all(da == 0) and torch.all(db == 0)
+    hq.hq_lora_backward(base, x, v, a, b, None, ends, da.fill_(3), db.fill_(3), accumulate=True, **kw)
+    assert torch.all(da == 3) and torch.all(db == 3)
