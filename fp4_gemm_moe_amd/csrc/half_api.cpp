@@ -100,10 +100,10 @@ hq_status check_lora_shape(const char* what, int64_t max_rows, int64_t n, int64_
 }
 
 // Checks common to both directions, after the shape's.
-hq_status check_lora(const char* what, const hq::LoraArgs& p, uint64_t need, uint64_t workspace_bytes) {
+hq_status check_lora(const char* what, const hq::LoraArgs& p, bool backward, uint64_t need, uint64_t workspace_bytes) {
   const hq::LoraPlan& pl = p.plan;
   if (pl.m < 0 || pl.m >= kMaxPlaces) return fail(HQ_ERR_SHAPE, "%s: m=%lld must be in [0, 2^30)", what, (long long)pl.m);
-  if (hq::lora_work_items(pl.max_rows, pl.m, p.n, p.k, p.r, pl.adapters) >= hq::kMaxWorkItems)
+  if (hq::lora_work_items(p, backward) >= hq::kMaxWorkItems)
     return fail(HQ_ERR_SHAPE, "%s: problem too large (a launch would pass 2^32 work items)", what);
   if ((pl.row_map != nullptr) != (pl.row_pair != nullptr) && pl.m > 0 && pl.max_rows > 0)
     return fail(HQ_ERR_NULL, "%s: row_map and row_pair go together", what);
@@ -254,7 +254,8 @@ hq_status hq_lora(void* stream, uint32_t flags, const uint16_t* x, const uint16_
   p.r = r;
   p.f16 = (flags & HQ_IN_FP16) != 0;
   p.workspace = workspace;
-  if ((st = check_lora(what, p, hq::lora_workspace_bytes(max_rows, n, k, r, num_adapters), workspace_bytes)) != HQ_OK)
+  if ((st = check_lora(what, p, false, hq::lora_workspace_bytes(max_rows, n, k, r, num_adapters), workspace_bytes)) !=
+      HQ_OK)
     return st;
   if (m == 0) return ok();
   if (!x || !a || !b || !out) return fail(HQ_ERR_NULL, "%s: x, a, b and out are required", what);
@@ -299,7 +300,7 @@ hq_status hq_lora_backward(void* stream, uint32_t flags, const uint16_t* dy, con
   p.db = db;
   p.accumulate = (flags & HQ_ACCUMULATE) != 0;
   p.workspace = workspace;
-  if ((st = check_lora(what, p, hq::lora_backward_workspace_bytes(max_rows, n, k, r, num_adapters),
+  if ((st = check_lora(what, p, true, hq::lora_backward_workspace_bytes(max_rows, n, k, r, num_adapters),
                        workspace_bytes)) != HQ_OK)
     return st;
   if (base != nullptr && dx == nullptr) return fail(HQ_ERR_NULL, "%s: base needs dx", what);

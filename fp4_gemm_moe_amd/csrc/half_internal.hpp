@@ -62,7 +62,7 @@ struct LoraArgs {
   bool accumulate;
   void* workspace;
 };
-int64_t lora_work_items(int64_t max_rows, int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters);
+int64_t lora_work_items(const LoraArgs& args, bool backward);
 uint64_t lora_workspace_bytes(int64_t max_rows, int64_t n, int64_t k, int64_t r, int32_t adapters);
 uint64_t lora_backward_workspace_bytes(int64_t max_rows, int64_t n, int64_t k, int64_t r, int32_t adapters);
 hipError_t launch_lora(hipStream_t s, const LoraArgs& args);

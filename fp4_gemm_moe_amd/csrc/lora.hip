@@ -1265,27 +1265,35 @@ hipError_t backward(hipStream_t s, const LoraArgs& p) {
 
 }  // namespace
 
-// The most work items of a launch of either direction.
-int64_t lora_work_items(int64_t max_rows, int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters) {
-  auto more = [](int64_t& most, int64_t wgs, int64_t threads) {
+// The most work items of a launch that the call makes.
+int64_t lora_work_items(const LoraArgs& p, bool backward) {
+  const LoraPlan& pl = p.plan;
+  int64_t most = 0;
+  auto launch = [&](int64_t wgs, int64_t threads) {
     const int64_t v = wgs < ((int64_t)1 << 40) ? wgs * threads : (int64_t)1 << 50;
     most = v > most ? v : most;
   };
-  int64_t most = 0;
-  const int64_t tiles = tile_bound(max_rows, adapters, expand_places(max_rows, adapters));
-  const int64_t places = outer_places(max_rows, n, k, r), chunks = tile_bound(max_rows, adapters, places);
-  for (const int64_t inner : {n, k}) {
-    const ShrinkPlan p = shrink_plan(max_rows, adapters, inner, r);
-    more(most, p.tiles * up(r, 16 * p.rf) * p.slices, kShrinkWaves * 64);
+  const int64_t inner = backward ? p.n : p.k, across = backward ? p.k : p.n;
+  const int64_t rest = p.base != p.out ? up(pl.m, kRestRows) * up(across, kRestCols) : 0;
+  if (!backward && one_launch(pl, p.n, p.k, p.r)) {
+    launch(tile_bound(pl.max_rows, pl.adapters, 16) * up(p.n, kOneWaves * 64) + rest, kOneWaves * 64);
+    return most;
   }
-  more(most, up(max_rows * r, 1024), 256);
-  more(most, kFill + up(m, kRestRows) * up(n, kRestCols), kOneWaves * 64);
-  for (const int64_t outer : {n, k}) {
-    const int64_t wgs = tiles * up(outer, expand_chunk(tiles, outer)) + up(m, kRestRows) * up(outer, kRestCols);
-    more(most, wgs, kThreads);
+  const ShrinkPlan plan = shrink_plan(pl.max_rows, pl.adapters, inner, p.r);
+  launch(plan.tiles * up(p.r, 16 * plan.rf) * plan.slices, plan.many ? 256 : kShrinkWaves * 64);
+  if (plan.summed()) launch(up(pl.max_rows * p.r, 1024), 256);
+  const int64_t tiles = tile_bound(pl.max_rows, pl.adapters, expand_places(pl.max_rows, pl.adapters));
+  const int64_t expand = tiles * up(across, expand_chunk(tiles, across)) + rest;
+  if (!backward) {
+    launch(expand, kThreads);
+    return most;
   }
-  more(most, chunks * up(r, 16 * outer_rf(r)) * (up(n, kOuterCols) + up(k, kOuterCols)), kThreads);
-  more(most, up(r * (k + n), 4 * kThreads) * adapters, kThreads);
+  const int64_t chunks = tile_bound(pl.max_rows, pl.adapters, outer_places(pl.max_rows, p.n, p.k, p.r));
+  const int64_t sums = chunks * up(p.r, 16 * outer_rf(p.r)) * (up(p.n, kOuterCols) + up(p.k, kOuterCols));
+  const bool dx = p.out != nullptr, joint = dx && sums + expand - rest <= 2 * kFill;
+  launch(joint ? sums + expand : sums, kThreads);
+  if (dx && !joint) launch(expand, kThreads);
+  launch(up(p.r * (p.k + p.n), 4 * kThreads) * pl.adapters, kThreads);
   return most;
 }
 
