@@ -1025,13 +1025,13 @@ __global__ __launch_bounds__(kThreads) void lora_sum(SumArgs p) {
   const int g = (int)(blockIdx.x / p.blocks);
   const int64_t at = ((int64_t)(blockIdx.x % p.blocks) * kThreads + threadIdx.x) * 4;
   const GroupTile t = group_tile<true>(p.pl.group_end, p.pl.adapters, (int)p.pl.max_rows, p.places, g);
-  const float f = sum_scale(p.pl, g, t.row0, t.row_end);
+  const int chunks = (t.row_end - t.row0 + p.places - 1) / p.places;
+  if (chunks == 1 || (p.accumulate && chunks == 0)) return;
+  const float f = chunks > 0 ? sum_scale(p.pl, g, t.row0, t.row_end) : 0.0f;      // by whole waves
   if (at >= p.na + p.nb) return;
   const bool b = at >= p.na;
   const int64_t n = b ? p.nb : p.na, i = b ? at - p.na : at;
-  const int chunks = (t.row_end - t.row0 + p.places - 1) / p.places;
   v4f* out = reinterpret_cast<v4f*>((b ? p.db : p.da) + g * n + i);
-  if (chunks == 1 || (p.accumulate && chunks == 0)) return;
   const float* src = (b ? p.pb : p.pa) + t.first * n + i;
   v4f s = {0, 0, 0, 0};
   for (int c = 0; c < chunks; ++c) s += *reinterpret_cast<const v4f*>(src + c * n);
