@@ -3,12 +3,10 @@
 
 #include <atomic>
 
+#include "half_plan.hpp"
 #include "half_tiled.hpp"
 
 namespace hq {
-
-// Tile shapes of the tiled kernel (rows x columns).
-enum HalfTile : int { kHalf256x256, kHalf128x256, kHalf128x128, kHalf64x128, kHalf32x64 };
 
 // One launch with the operands as the products have them: a and b K-minor (nt),
 // b K-major outside (nn), both (tn, the form that sums over the groups' rows).

@@ -1,4 +1,4 @@
-// The tiled 16-bit GEMM kernel (half_gemm.hip picks the shape; half_nt.hip, half_nn.hip
+// The tiled 16-bit GEMM kernel (half_plan.hpp picks the shape; half_nt.hip, half_nn.hip
 // and half_tn.hip instantiate it).
 //
 // out = sum over k of a b, per tile in FP32 on the matrix cores (products of 16-bit
