@@ -48,17 +48,17 @@ hipError_t launch_type(hipStream_t s, const HalfGemmArgs& p, const DeviceInfo& d
   return p.f16 ? launch_one<C, AT, BT, true>(s, p, dev) : launch_one<C, AT, BT, false>(s, p, dev);
 }
 
+// The tiles that plan_half has for the form: sums over the rows take two of them.
 template <bool AT, bool BT>
 hipError_t launch_tile(hipStream_t s, const HalfGemmArgs& p, const DeviceInfo& dev, int tile) {
-  switch (tile) {
-    case kHalf256x256: return launch_type<Cfg<256, 256, 2, 2, 2>, AT, BT>(s, p, dev);
-    case kHalf128x256:
-      if constexpr (!AT) return launch_type<Cfg<128, 256, 2, 2, 2>, AT, BT>(s, p, dev);
-      return hipErrorInvalidValue;       // not planned for sums over the rows
-    case kHalf128x128: return launch_type<Cfg<128, 128, 2, 2, 4>, AT, BT>(s, p, dev);
-    case kHalf64x128: return launch_type<Cfg<64, 128, 1, 4, 5>, AT, BT>(s, p, dev);
-    default: return launch_type<Cfg<32, 64, 1, 2, 9>, AT, BT>(s, p, dev);
+  if (tile == kHalf256x256) return launch_type<Cfg<256, 256, 2, 2, 2>, AT, BT>(s, p, dev);
+  if (tile == kHalf128x128) return launch_type<Cfg<128, 128, 2, 2, 4>, AT, BT>(s, p, dev);
+  if constexpr (!AT) {
+    if (tile == kHalf128x256) return launch_type<Cfg<128, 256, 2, 2, 2>, AT, BT>(s, p, dev);
+    if (tile == kHalf64x128) return launch_type<Cfg<64, 128, 1, 4, 5>, AT, BT>(s, p, dev);
+    if (tile == kHalf32x64) return launch_type<Cfg<32, 64, 1, 2, 9>, AT, BT>(s, p, dev);
   }
+  return hipErrorInvalidValue;           // no such plan
 }
 
 }  // namespace half

@@ -2,11 +2,13 @@
 own rules (csrc/half_plan.hpp) says what each size of _half_plans.py takes on 256
 compute units, and that no kernel, result type or store policy is left without one."""
 import os
+import re
 import shutil
 import subprocess
 
 import pytest
 
+import fp4_gemm_moe_amd as hq
 from fp4_gemm_moe_amd import build
 from tests import _half_plans as P
 
@@ -89,3 +91,17 @@ def test_every_variant_has_a_size(planned):
                 want.add((form, False, t, out, "direct"))
             want |= {(GROUP_K, False, t, out, f"{tile} {policy}") for tile in ("256x256", "128x128")}
     assert seen == want
+
+
+def test_every_kernel_that_is_built_has_a_size(planned):
+    """The tiled kernels in the library are those that the plans take."""
+    if shutil.which("nm") is None:
+        pytest.skip("no symbol reader")
+    if not os.path.exists(hq.library_path()):
+        build.build(verbose=False)
+    names = subprocess.run(["nm", "-C", hq.library_path()], capture_output=True, text=True, check=True).stdout
+    built = {(f"{m[1]}x{m[2]}", m[3] == "true", m[4] == "true", m[5] == "true") for m in re.finditer(
+        r"__device_stub__half_gemm_tiled<hq::half::Cfg<(\d+), (\d+)[^>]*>, (\w+), (\w+), (\w+)>", names)}
+    sizes = ([(False, c[-2], c[-4]) for c in P.CONTIGUOUS + P.MASKED] + [(True, True, c[-3]) for c in P.GROUP_K])
+    taken = {(plan.split()[0], at, bt, t == "fp16") for (at, bt, t), plan in zip(sizes, planned) if plan != "direct"}
+    assert built == taken
