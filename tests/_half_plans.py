@@ -74,3 +74,7 @@ _SUMS = [
 ]
 GROUP_K = [(c, spare, m, n, t, out, f"{tile} p{int(p and out != 'add')}")
            for c, spare, m, n, tile, p in _SUMS for t, out in KINDS]
+
+# groups of many thousands of rows, the last of them past 2^31 elements of a
+GROUP_K += [([450000, 0, 449999, 70001], 7, 2560, 1536, t, out, "256x256 " + ("p0" if out == "add" else "p1"))
+            for t, out in (("bf16", "f32"), ("fp16", "add"))]
