@@ -8,10 +8,16 @@
 // cycle) needs half of the matrix cores' time; with 128x128 tiles all of it, which
 // those pay with 0.37 of a large tile's time for a quarter of its work.  Operands
 // go straight to LDS, 64 K values a step, two steps ahead (large tiles) to nine.
-// Bound: matrix cores at the clock that power leaves.  65536 rows of 32 experts, 4096
-// x 1536: 675 us, 1.22 PFLOP/s (a library's dense product of this size 687 us; with all
-// operands zero this kernel takes 614 us), b transposed 683 us, the weights'
-// sums over rows (both operands read transposed from LDS, 805 MB of results) 715 us.
+// 65536 rows of 32 experts, 4096 x 1536: 673 to 711 us by card, 1.16 to 1.23 PFLOP/s (a
+// library's dense product of this size 687 us), b transposed 683 to 718 us, the weights'
+// sums over rows (both operands read transposed from LDS, 805 MB of results) 713 to
+// 740 us.  Bound: the matrix cores are busy for 55 to 61 % of the cycles at the 1.9 GHz
+// that power leaves (all operands zero: 614 us of 675); the rest of the cycles is a
+// tile's fill and epilogue, with one workgroup a unit to cover them.
+// Accumulated FP32 results are the slow ones: each share of a tile is loaded, waited
+// for, added to and stored before the next one's load, a chain of trips to memory:
+// 1216 us where plain FP32 results take 758, sums over rows 1046 and 713, and 303 and
+// 88 where a group has 128 rows (32 groups, 2048 x 1536).
 // Against it: 32x32x16 fragments 3-5 % slower (2.5 % faster on zeros), steps of 32 K
 // values in four stages 777 us, loads bunched at a half's start 4 % slower.
 #pragma once

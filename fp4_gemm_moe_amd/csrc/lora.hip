@@ -988,7 +988,8 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& p, int id) {
 // dA's and dB's chunks in one launch; where they are few, dx's tiles too (its
 // registers would keep the chunks from filling the chip; three workgroups a compute
 // unit where 16 ranks allow it: 2918 tokens, 1568 + 1344 wide, 33.0 -> 28.6 us, while
-// dx alone is better off with two, 4096 places of 17408 columns 76 us against 81).
+// dx alone is better off with two, 4096 places of 17408 columns 76 us against 81; the
+// bound costs lora_back<., 1, true> four to six spilled registers, inside that gain).
 struct BackArgs {
   OuterArgs da, db;
   ExpandArgs dx;
@@ -1049,7 +1050,10 @@ int64_t tile_bound(int64_t max_rows, int64_t adapters, int64_t bm) {
 }
 constexpr int64_t kFill = 512;           // workgroups that fill the chip
 
-// Few places an adapter on average: tiles of 16, more of 64.
+// Few places an adapter on average: tiles of 16, more of 64.  The average is over all
+// adapters, since only the device knows which of them have tokens: 1000 tokens of two
+// adapters, 4096 x 4096, take 25.4 us with 64 adapters of rank 64 loaded and 19.4 with two
+// (5120 x 5120, rank 16: 14.3 and 15.8).
 struct ShrinkPlan {
   bool many;
   int rf, slices;

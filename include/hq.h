@@ -663,8 +663,8 @@ hq_status hq_moe_combine_backward(void* stream, const uint16_t* dout, const uint
  * hq_half_group_k_gemm: out[g] = sum over the rows r of group g of a[r]^T b[r];
  *   a [rows, m], b [rows, n], out [num_groups, m, n]: the gradient for the
  *   weights of a contiguous product, from its operands as they are.  Groups may
- *   have any size; one without rows gives zeros (leaves out as it is with
- *   HQ_ACCUMULATE).
+ *   have any size; one without rows gives zeros (with HQ_ACCUMULATE its result is
+ *   neither read nor written).
  */
 hq_status hq_half_group_contiguous_gemm(void* stream, uint32_t flags, const uint16_t* a,
                                         const uint16_t* b, const int32_t* group_end,
@@ -684,9 +684,9 @@ hq_status hq_half_group_k_gemm(void* stream, uint32_t flags, const uint16_t* a,
  * (BF16, FP16 with HQ_IN_FP16), s = 1 / (1 + exp(-gate)),
  *   y     = up gate s                               [rows, h]
  *   dgate = dy up s (1 + gate (1 - s)),  dup = dy gate s,  dx = [dgate | dup]
- * in FP32, rounded once.  The gradient also writes y again where y is not NULL
- * (the operand of the down projection's weights' gradient, which then need not
- * be kept).
+ * in FP32, rounded once (exp(-|gate|) below 2^-126 may count as zero).  The
+ * gradient also writes y again where y is not NULL (the operand of the down
+ * projection's weights' gradient, which then need not be kept).
  * Row selection as in hq_fused_swiglu_quant, with num_groups == 0 (group_end and
  * valid NULL) for all rows; rows that are not selected are neither read nor
  * written.  h % 8 == 0, h < 2^27; x, y, dy and dx 16-byte aligned, group_end and
@@ -745,9 +745,11 @@ hq_status hq_swiglu_backward(void* stream, const uint16_t* dy, const uint16_t* x
  *   db[g] = scale[g] sum over g's tokens of dy[t]^T v[t]     [num_adapters, n, r] FP32
  * base [m, k] is the gradient for x through the projection, read and written as
  * above (it may be dx); dx NULL: it is not computed (base is then NULL too).  With
- * HQ_ACCUMULATE da and db are added to.  An adapter without tokens gets zeros (is
- * left as it is).  The sums' order is fixed: results do not vary from run to run.
- * The workspace holds hq_lora_backward_workspace_size bytes.
+ * HQ_ACCUMULATE da and db are added to.  An adapter without tokens gets zeros, whatever
+ * its scale (zeros are added; without places nothing is read or written).  The sums'
+ * order is fixed: results do not vary from run to run.  The workspace holds
+ * hq_lora_backward_workspace_size bytes, among them r (k + n) floats for every
+ * adapter that may have places.
  */
 hq_status hq_lora(void* stream, uint32_t flags, const uint16_t* x, const uint16_t* a,
                   const uint16_t* b, const float* scale, const int32_t* group_end,
